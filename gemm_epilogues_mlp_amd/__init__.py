@@ -30,6 +30,10 @@ __all__ = [
     "swiglu_pack_fragments", "VARIANT_FP8_PACKED", "swiglu_fp8_packed_bytes",
     "swiglu_pack_fp8_fragments", "VARIANT_MXFP8_PACKED", "swiglu_forward_mx_packed",
     "swiglu_mx_packed_bytes", "swiglu_pack_mx_fragments",
+    "DTYPE_BF16", "DTYPE_F32", "swiglu_route_workspace_bytes", "swiglu_route",
+    "swiglu_grouped_forward", "swiglu_grouped_matmul", "swiglu_combine_norm",
+    "swiglu_mxfp4_bytes", "swiglu_mxfp4_scale_bytes", "swiglu_quantize_mxfp4",
+    "swiglu_dequantize_mxfp4", "swiglu_forward_mxfp4",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +44,7 @@ LAYOUT_SEPARATE, LAYOUT_INTERLEAVED, LAYOUT_PACKED = 0, 1, 2
 VARIANT_AUTO, VARIANT_SYNC, VARIANT_INTERLEAVE, VARIANT_GEMM, VARIANT_FP8, VARIANT_FP8_SYNC, \
     VARIANT_MXFP8, VARIANT_PACKED, VARIANT_FP8_PACKED, VARIANT_MXFP8_PACKED, VARIANT_MXFP8_SYNC, \
     VARIANT_PACKED_SPLITK = 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11
+DTYPE_BF16, DTYPE_F32 = 0, 1
 
 
 class SwiGLUError(RuntimeError):
@@ -118,6 +123,17 @@ def load():
         "swiglu_packed_splitk_plan": ([p, i64, i64, i64, ctypes.POINTER(i32),
                                        ctypes.POINTER(i32)], st),
         "swiglu_forward_packed_splitk": ([p, p, p, p, i64, i64, i64, i32, i32, p, i64, p], st),
+        "swiglu_route_workspace_bytes": ([i64, i64, i64], i64),
+        "swiglu_route": ([p, p, p, p, p, p, p, i64, i64, i64, i64, i32, ctypes.c_int, p], st),
+        "swiglu_grouped_forward": ([p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, i32, p], st),
+        "swiglu_grouped_matmul": ([p, p, p, p, p, p, i64, i64, i64, i64, i32, p], st),
+        "swiglu_combine_norm": ([p, p, p, p, p, p, p, p, p, p, p, i64, i64, i64, ctypes.c_float,
+                                 ctypes.c_float, i64, ctypes.c_int, p], st),
+        "swiglu_mxfp4_bytes": ([i64, i64], i64),
+        "swiglu_mxfp4_scale_bytes": ([i64, i64], i64),
+        "swiglu_quantize_mxfp4": ([p, p, p, p, i64, i64, p], st),
+        "swiglu_dequantize_mxfp4": ([p, p, p, p, i64, i64, p], st),
+        "swiglu_forward_mxfp4": ([p, p, p, p, p, p, i64, i64, i64, i32, p], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -346,6 +362,76 @@ def swiglu_query_fp8(handle, M, N, K, variant=VARIANT_AUTO):
     _check(load().swiglu_query_fp8(handle, M, N, K, variant, ctypes.byref(t)),
            "swiglu_query_fp8")
     return t.as_dict()
+
+
+# ---- mixture of experts ---------------------------------------------------------
+def swiglu_route_workspace_bytes(T: int, E: int, k: int) -> int:
+    return int(load().swiglu_route_workspace_bytes(T, E, k))
+
+
+def swiglu_route(handle, logits, weights, experts, offsets, rows, workspace, T, E, k,
+                 renormalize=True, dtype=DTYPE_F32, stream=None):
+    """The k largest of each token's E logits, their weights, and the T k slots
+    sorted by expert; `workspace`: a byte tensor of swiglu_route_workspace_bytes
+    (or None where that is 0)."""
+    _check(load().swiglu_route(handle, _ptr(logits), _ptr(weights), _ptr(experts), _ptr(offsets),
+                               _ptr(rows), _ptr(workspace),
+                               0 if workspace is None else
+                               workspace.numel() * workspace.element_size(),
+                               T, E, k, 1 if renormalize else 0, dtype, _stream(stream)),
+           "swiglu_route")
+
+
+def swiglu_grouped_forward(handle, A, rows, offsets, W, Y, T, R, N, K, E, k=1, variant=-1,
+                           stream=None):
+    """Gated products of the sorted rows: A [T, K] gathered by rows // k, W [E, K, 2N]
+    (W_fused order), Y [R, N] in sorted order."""
+    _check(load().swiglu_grouped_forward(handle, _ptr(A), _ptr(rows), _ptr(offsets), _ptr(W),
+                                         _ptr(Y), T, R, N, K, E, k, variant, _stream(stream)),
+           "swiglu_grouped_forward")
+
+
+def swiglu_grouped_matmul(handle, A, rows, offsets, W, Y, R, N, K, E, variant=-1, stream=None):
+    """Y[rows[i]] = A[i] W_e: A [R, K] in sorted order, W [E, K, N], Y in slot order."""
+    _check(load().swiglu_grouped_matmul(handle, _ptr(A), _ptr(rows), _ptr(offsets), _ptr(W),
+                                        _ptr(Y), R, N, K, E, variant, _stream(stream)),
+           "swiglu_grouped_matmul")
+
+
+def swiglu_combine_norm(handle, B, weights, experts, S, X, post, gate, pre, X_out, H, T, D, k=1,
+                        scale=1.0, eps=1e-6, gate_ld=0, dtype=DTYPE_BF16, stream=None):
+    """X_out = X + scale gate norm(sum_j w_j B_j + S) post, H = norm(X_out) pre; S, post and
+    gate may be None, dtype is X's."""
+    _check(load().swiglu_combine_norm(handle, _ptr(B), _ptr(weights), _ptr(experts), _ptr(S),
+                                      _ptr(X), _ptr(post), _ptr(gate), _ptr(pre), _ptr(X_out),
+                                      _ptr(H), T, D, k, scale, eps, gate_ld, dtype,
+                                      _stream(stream)), "swiglu_combine_norm")
+
+
+# ---- MXFP4 ------------------------------------------------------------------------
+def swiglu_mxfp4_bytes(rows: int, K: int) -> int:
+    return int(load().swiglu_mxfp4_bytes(rows, K))
+
+
+def swiglu_mxfp4_scale_bytes(rows: int, K: int) -> int:
+    return int(load().swiglu_mxfp4_scale_bytes(rows, K))
+
+
+def swiglu_quantize_mxfp4(handle, X, Q, S, rows, K, stream=None):
+    """bf16 X [rows, K] -> fragment-ordered codes Q and scales S."""
+    _check(load().swiglu_quantize_mxfp4(handle, _ptr(X), _ptr(Q), _ptr(S), rows, K,
+                                        _stream(stream)), "swiglu_quantize_mxfp4")
+
+
+def swiglu_dequantize_mxfp4(handle, Q, S, X, rows, K, stream=None):
+    _check(load().swiglu_dequantize_mxfp4(handle, _ptr(Q), _ptr(S), _ptr(X), rows, K,
+                                          _stream(stream)), "swiglu_dequantize_mxfp4")
+
+
+def swiglu_forward_mxfp4(handle, Q, SQ, W, SW, Y, M, N, K, variant=-1, stream=None):
+    """Y [M, N] of activations (Q, SQ) [M, K] and paired weights (W, SW) [2N, K] in MXFP4."""
+    _check(load().swiglu_forward_mxfp4(handle, _ptr(Q), _ptr(SQ), _ptr(W), _ptr(SW), _ptr(Y), M,
+                                       N, K, variant, _stream(stream)), "swiglu_forward_mxfp4")
 
 
 def swiglu_config_count() -> int:

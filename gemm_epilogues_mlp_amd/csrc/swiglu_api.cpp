@@ -30,6 +30,10 @@ struct swiglu_ctx {
   void* scratch;  // this device's copy of the fixed scratch array (device address)
 };
 
+namespace swiglu {
+int handle_device(const ::swiglu_ctx* h) { return h->device; }
+}  // namespace swiglu
+
 // ---- fixed device scratch for callers that cannot allocate -------------------
 // swiglu_forward_unfused_static keeps the unfused baseline's bf16 Gate and Up
 // tensors here instead of in a caller workspace.  One copy per device, held

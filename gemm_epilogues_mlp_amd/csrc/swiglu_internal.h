@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+struct swiglu_ctx;  // the handle
+
 namespace swiglu {
 
 // VAR_F8 / VAR_F8_SYNC: interleave / sync order on FP8 (E4M3) inputs with
@@ -104,6 +106,54 @@ hipError_t launch_pack_frag(const uint16_t* W1, const uint16_t* W2, uint16_t* P,
                            hipStream_t stream, int cu_count);
 hipError_t launch_pack_kmajor(const uint16_t* W1, const uint16_t* W2, uint16_t* Wt, int N, int K,
                               hipStream_t stream, int cu_count);
+
+// Device of a handle (swiglu_api.cpp).
+int handle_device(const ::swiglu_ctx* h);
+
+// ---- mixture-of-experts operators (swiglu_route.hip, swiglu_grouped.hip,
+// swiglu_norm.hip); sizes are checked by the caller -----------------------------
+constexpr long long kMaxExperts = 1024, kMaxChoices = 64, kMaxNormWidth = 16384;
+long long route_workspace_bytes(long long T, long long E, long long k);
+hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* experts,
+                        int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
+                        bool renorm, hipStream_t stream);
+// Grouped products; TA: rows of A, variant < 0: by rule
+constexpr int kGroupedVariants = 5;
+hipError_t launch_grouped(bool up, const uint16_t* A, const int32_t* rows, const int32_t* offsets,
+                          const uint16_t* W, uint16_t* Y, int TA, int R, int N, int K, int E,
+                          int k, int variant, hipStream_t stream);
+struct NormCall {
+  const void* B;
+  const float* weights;
+  const int32_t* experts;
+  const void *S, *X, *post, *gate, *pre;  // S, post, gate may be null
+  void *X_out, *H;
+  long long T, D, k;
+  float scale, eps;
+  long long gate_ld;
+  bool f32;  // X and X_out
+};
+hipError_t launch_combine_norm(const NormCall& c, hipStream_t stream);
+
+// ---- MXFP4 (swiglu_fp4.hip) ----------------------------------------------------
+// Bytes of the codes and of the scales of [rows, K] in fragment order.
+inline long long fp4_code_bytes(long long rows, long long K) {
+  return (rows + 31) / 32 * ((K + 255) / 256) * 4096;
+}
+inline long long fp4_scale_bytes(long long rows, long long K) {
+  return (rows + 31) / 32 * ((K + 255) / 256) * 256;
+}
+struct Fp4Call {
+  const uint8_t *A, *SA, *W, *SW;
+  uint16_t* Y;
+  long long M, N, K;
+};
+constexpr int kFp4Variants = 5;
+hipError_t launch_forward_mxfp4(const Fp4Call& c, int variant, hipStream_t stream);
+hipError_t launch_quantize_mxfp4(const uint16_t* X, uint8_t* Q, uint8_t* S, int rows, int K,
+                                 hipStream_t stream);
+hipError_t launch_dequantize_mxfp4(const uint8_t* Q, const uint8_t* S, uint16_t* X, int rows,
+                                   int K, hipStream_t stream);
 
 // Per-shape choice (tile table + fallback rule).  variant is SYNC, INTERLEAVE
 // or GEMM; returns a config id of that variant.

@@ -1,0 +1,219 @@
+// swiglu_norm.hip -- the end of a block: the experts' outputs of a token summed
+// with their weights, a norm behind the block, its gate and residual scale,
+// and the norm in front of the next block, in one pass.
+//
+// For token t (experts[t, j] < 0: that row of B is not read into the sum,
+// whatever it holds):
+//   o = sum_j weights[t, j] B[t k + j] + S[t]
+//   o = o / sqrt(mean(o^2) + eps) * post        (post given)
+//   o = o * gate                                (a row [D], or one a token)
+//   x = X[t] + scale o                          -> X_out
+//   h = x / sqrt(mean(x^2) + eps) * pre         -> H (bf16)
+// Everything between loads and stores is fp32 (the second norm takes x before
+// its rounding); each input is read once, so the memory bounds it.
+//
+// A token's D values stay in registers: NW waves of it, VPL vectors of 8 a
+// lane.  Many tokens: one wave each (no barrier, k VPL 16-byte loads in flight
+// a lane); few tokens: as many waves as D has, for latency.
+#include "swiglu_internal.h"
+#include "swiglu_ops_device.hpp"
+
+namespace swiglu {
+
+struct NormArgs {
+  const uint16_t* B;
+  const float* weights;
+  const int32_t* experts;
+  const uint16_t* S;
+  const void* X;
+  const uint16_t* post;
+  const uint16_t* gate;
+  const uint16_t* pre;
+  void* X_out;
+  uint16_t* H;
+  int T, D, k;
+  float scale, eps;
+  long long gate_ld;  // 0: one row for all tokens
+};
+
+__device__ __forceinline__ void unpack8(const u32x4& v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __builtin_bit_cast(float, v[i] << 16);
+    f[2 * i + 1] = __builtin_bit_cast(float, v[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+               pack_bf16x2(f[6], f[7])};
+}
+
+// Sum over the NW waves of a token; `part` is LDS of its own for this call.
+template <int NW>
+__device__ __forceinline__ float token_sum(float v, float* part) {
+  v = group_sum<64>(v);
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += part[w];
+  }
+  return v;
+}
+
+template <bool XF32, int NW, int VPL>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void combine_norm_kernel(NormArgs a) {
+  __shared__ __attribute__((aligned(16))) float part[2 * NW];
+  constexpr int kPer = NW == 1 ? 4 : 1;  // tokens of a workgroup
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = __builtin_amdgcn_readfirstlane((int)blockIdx.x * kPer + (NW == 1 ? wave : 0));
+  if (t >= a.T) return;  // NW > 1: the whole workgroup
+  const int l0 = NW == 1 ? lane : (int)threadIdx.x;
+  const int nv = a.D / 8;
+
+  bool in[VPL];
+  size_t at[VPL];  // element offset in a row; past the row: the last vector, not stored
+  float o[VPL][8];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int c = l0 + v * 64 * NW;
+    in[v] = c < nv;
+    at[v] = (size_t)min(c, nv - 1) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[v][i] = 0.0f;
+  }
+  const uint16_t* B = a.B + (size_t)t * a.k * a.D;
+  auto add = [&](const u32x4 (&b)[VPL], int j) __attribute__((always_inline)) {
+    const bool there = a.experts[(size_t)t * a.k + j] >= 0;
+    const float w = there ? a.weights[(size_t)t * a.k + j] : 0.0f;
+    const uint32_t keep = there ? 0xffffffffu : 0u;  // a row nobody wrote may hold NaN
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      float f[8];
+      unpack8(b[v] & keep, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[v][i] = fmaf(w, f[i], o[v][i]);
+    }
+  };
+  auto fetch = [&](u32x4 (&b)[VPL], int j) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) b[v] = load16_stream(B + (size_t)j * a.D + at[v]);
+  };
+  constexpr int kAhead = VPL <= 2 ? 4 : 2;  // rows of B loaded together
+  int j = 0;
+  for (; j + kAhead <= a.k; j += kAhead) {
+    u32x4 b[kAhead][VPL];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) fetch(b[q], j + q);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) add(b[q], j + q);
+  }
+  for (; j < a.k; ++j) {
+    u32x4 b[VPL];
+    fetch(b, j);
+    add(b, j);
+  }
+  if (a.S) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      float f[8];
+      unpack8(load16(a.S + (size_t)t * a.D + at[v]), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[v][i] += f[i];
+    }
+  }
+  if (a.post) {
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += in[v] ? o[v][i] * o[v][i] : 0.0f;
+    const float r = rsqrtf(token_sum<NW>(s, part) / (float)a.D + a.eps);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      float f[8];
+      unpack8(load16(a.post + at[v]), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[v][i] *= r * f[i];
+    }
+  }
+  if (a.gate) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      float f[8];
+      unpack8(load16(a.gate + (size_t)t * a.gate_ld + at[v]), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[v][i] *= f[i];
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const size_t p = (size_t)t * a.D + at[v];
+    float x[8];
+    if constexpr (XF32) {
+      const f32x4 lo = __builtin_bit_cast(f32x4, load16((const float*)a.X + p));
+      const f32x4 hi = __builtin_bit_cast(f32x4, load16((const float*)a.X + p + 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
+    } else {
+      unpack8(load16((const uint16_t*)a.X + p), x);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[v][i] = fmaf(a.scale, o[v][i], x[i]);
+      s += in[v] ? o[v][i] * o[v][i] : 0.0f;
+    }
+    if (in[v]) {
+      if constexpr (XF32) {
+        float* out = (float*)a.X_out + p;
+        *reinterpret_cast<f32x4*>(out) = f32x4{o[v][0], o[v][1], o[v][2], o[v][3]};
+        *reinterpret_cast<f32x4*>(out + 4) = f32x4{o[v][4], o[v][5], o[v][6], o[v][7]};
+      } else {
+        *reinterpret_cast<u32x4*>((uint16_t*)a.X_out + p) = pack8(o[v]);
+      }
+    }
+  }
+  const float r = rsqrtf(token_sum<NW>(s, part + NW) / (float)a.D + a.eps);
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    float f[8];
+    unpack8(load16(a.pre + at[v]), f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= r * o[v][i];
+    if (in[v]) *reinterpret_cast<u32x4*>(a.H + (size_t)t * a.D + at[v]) = pack8(f);
+  }
+}
+
+template <bool XF32, int NW, int VPL>
+static hipError_t launch_norm_as(const NormArgs& a, hipStream_t stream) {
+  const int per = NW == 1 ? 4 : 1;
+  return launch_op(combine_norm_kernel<XF32, NW, VPL>, dim3((a.T + per - 1) / per),
+                   dim3(NW == 1 ? 256 : 64 * NW), stream, a);
+}
+
+template <bool XF32>
+static hipError_t launch_norm_x(const NormArgs& a, hipStream_t stream) {
+  const int nv = a.D / 8;  // at most 2048
+  if (a.T >= 1024) {
+    if (nv <= 64) return launch_norm_as<XF32, 1, 1>(a, stream);
+    if (nv <= 128) return launch_norm_as<XF32, 1, 2>(a, stream);
+    if (nv <= 192) return launch_norm_as<XF32, 1, 3>(a, stream);
+    if (nv <= 256) return launch_norm_as<XF32, 1, 4>(a, stream);
+  }
+  if (nv <= 256) return launch_norm_as<XF32, 4, 1>(a, stream);
+  if (nv <= 512) return launch_norm_as<XF32, 8, 1>(a, stream);
+  if (nv <= 1024) return launch_norm_as<XF32, 8, 2>(a, stream);
+  return launch_norm_as<XF32, 16, 2>(a, stream);
+}
+
+hipError_t launch_combine_norm(const NormCall& c, hipStream_t stream) {
+  const NormArgs a{(const uint16_t*)c.B,    c.weights, c.experts, (const uint16_t*)c.S,
+                   c.X,                     (const uint16_t*)c.post, (const uint16_t*)c.gate,
+                   (const uint16_t*)c.pre,  c.X_out,   (uint16_t*)c.H, (int)c.T, (int)c.D,
+                   (int)c.k,                c.scale,   c.eps,     c.gate_ld};
+  return c.f32 ? launch_norm_x<true>(a, stream) : launch_norm_x<false>(a, stream);
+}
+
+}  // namespace swiglu

@@ -1,0 +1,333 @@
+// swiglu_route.hip -- the router of a mixture-of-experts block: which experts a
+// token goes to and with what weight, and the order that puts the tokens of an
+// expert next to each other.
+//
+// For token t with logits x (E of them, -inf or NaN: masked off), the chosen
+// experts are the k largest logits, the lowest index first among equals, and
+//   weight_i = exp(x_i - m) / S,  m = max x,
+//   S = sum of exp(x_j - m) over the chosen ones (renormalize) or over all E.
+// A token with fewer than k open experts has -1 and weight 0 in the places
+// left over.  Slot t k + i then belongs to expert experts[t, i]; the slots
+// sorted by (expert, slot) are `rows`, expert e's at [offsets[e],
+// offsets[e + 1]), and -1 fills what follows offsets[E].
+//
+// The work is a few operations a logit: a call is bound by its launches and by
+// the latency of its memory accesses.  Up to kRouteSmall slots one workgroup
+// does all of it in one launch; beyond that one launch chooses and counts, a
+// second one places.  The order comes from counts and ranks, never from the
+// arrival of atomics, so it is the same in every run.
+#include "swiglu_internal.h"
+#include "swiglu_ops_device.hpp"
+
+namespace swiglu {
+
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ float logit_value(float x) { return x == x ? x : kNegInf; }
+
+// C logits of the lane: indices [C gl, C gl + C) of a row of E.
+template <int C>
+__device__ __forceinline__ void load_logits(const float* row, int E, int i0, bool vec,
+                                            float (&x)[C]) {
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < C; j += 4) {
+      const bool in = i0 + j < E;  // E % 4 == 0
+      const f32x4 v = __builtin_bit_cast(f32x4, in ? load16(row + i0 + j) : u32x4{0, 0, 0, 0});
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[j + q] = in ? logit_value(v[q]) : kNegInf;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) x[j] = i0 + j < E ? logit_value(row[i0 + j]) : kNegInf;
+  }
+}
+template <int C>
+__device__ __forceinline__ void load_logits(const uint16_t* row, int E, int i0, bool vec,
+                                            float (&x)[C]) {
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < C; j += 8) {
+      const bool in = i0 + j < E;  // E % 8 == 0
+      const u32x4 v = in ? load16(row + i0 + j) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        x[j + q] = in ? logit_value(bf16_to_float((uint16_t)(v[q / 2] >> (16 * (q & 1))))) : kNegInf;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      x[j] = i0 + j < E ? logit_value(bf16_to_float(row[i0 + j])) : kNegInf;
+  }
+}
+
+struct RouteArgs {
+  const void* logits;
+  float* weights;
+  int32_t* experts;
+  int32_t* offsets;
+  int32_t* rows;
+  int32_t* counts;  // workspace: [blocks, E]
+  int T, E, k, renorm;
+  int vec;          // rows are 16-byte aligned and a multiple of 16 bytes
+  int tokens;       // tokens of a workgroup
+};
+
+// The experts of one token on G lanes (C logits each; lane order is index
+// order, so the lowest of several equal maxima is in the lowest lane that has
+// one).  Every lane takes part in the cross-lane steps; `in` says whether the
+// token exists.  Lane gl < k keeps choice gl, for k <= G.
+template <typename In, int G, int C>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, bool in, int32_t& expert,
+                                            float& weight) {
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  float x[C];
+  load_logits<C>((const In*)a.logits + (size_t)(in ? t : 0) * a.E, in ? a.E : 0, gl * C, a.vec, x);
+  float top = 0.0f, total = 0.0f;
+  expert = -1;
+  weight = 0.0f;
+  for (int i = 0; i < a.k; ++i) {
+    float v = x[0];
+    int bj = 0;
+#pragma unroll
+    for (int j = 1; j < C; ++j)
+      if (x[j] > v) v = x[j], bj = j;
+    const float best = group_max<G>(v);
+    const bool open = best > kNegInf;
+    if (i == 0) {
+      // all E terms, before any is taken out; an infinite maximum (equal
+      // shares of what is infinite) has no finite difference to itself
+      top = open ? best : 0.0f;
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C; ++j) s += x[j] == top ? 1.0f : expf(x[j] - top);
+      total = a.renorm ? 0.0f : group_sum<G>(open ? s : 0.0f);
+    }
+    const unsigned long long group = (G == 64 ? ~0ull : ((1ull << (G & 63)) - 1)) << (lane & ~(G - 1));
+    const int src = __ffsll(__ballot(v == best) & group) - 1;
+    const int idx = __shfl(gl * C + bj, src);
+    const float p = !open ? 0.0f : (best == top ? 1.0f : expf(best - top));
+    if (a.renorm) total += p;
+    if (gl == i) expert = open ? idx : -1, weight = p;
+    if (lane == src) {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j == bj) x[j] = kNegInf;
+    }
+  }
+  weight = total > 0.0f ? weight / total : 0.0f;
+}
+
+// Tokens [t0, t1) by the workgroup: results to memory, slots counted in hist.
+template <typename In, int G, int C>
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, int t0, int t1, int* hist) {
+  const int per = blockDim.x / G, gl = threadIdx.x & (G - 1);
+  for (int t = t0 + (int)threadIdx.x / G; t - (int)threadIdx.x / G < t1; t += per) {
+    const bool in = t < t1;
+    int32_t e;
+    float w;
+    route_token<In, G, C>(a, t, in, e, w);
+    if (in && gl < a.k) {
+      a.experts[(size_t)t * a.k + gl] = e;
+      a.weights[(size_t)t * a.k + gl] = w;
+      if (e >= 0) atomicAdd(hist + e, 1);
+    }
+  }
+}
+
+// Lanes of the wave with the same expert as this one.
+__device__ __forceinline__ unsigned long long same_expert(int e, int E) {
+  unsigned long long m = ~0ull;
+  for (int b = 1; b <= E; b <<= 1) {  // -1 counts as E
+    const unsigned long long one = __ballot((e < 0 ? E : e) & b);
+    m &= ((e < 0 ? E : e) & b) ? one : ~one;
+  }
+  return m;
+}
+
+// Slots [s0, s1) into their places: `next` holds, for every wave and expert,
+// the next free place (already advanced past the earlier slots).
+__device__ __forceinline__ void route_place(const RouteArgs& a, int s0, int s1, int total, int* next) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  const int per = ((s1 - s0 + nw - 1) / nw + 63) / 64 * 64;
+  const int b = s0 + wave * per, e = min(b + per, s1);
+  const int n = a.T * a.k;
+  int* mine = next + wave * a.E;
+  for (int s = b + lane; s - lane < e; s += 64) {
+    const int x = s < e ? a.experts[s] : -1;
+    const unsigned long long same = same_expert(x, a.E);
+    if (x >= 0 && x < a.E) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      const int at = mine[x] + rank;
+      if (at >= 0 && at < n) a.rows[at] = s;
+      if (rank == 0) mine[x] += __popcll(same);
+    }
+  }
+  for (int s = s0 + (int)threadIdx.x; s < s1; s += blockDim.x)
+    if (s >= total) a.rows[s] = -1;
+}
+
+// Counts of each wave's share of [s0, s1) into next[wave][expert].
+__device__ __forceinline__ void route_count(const RouteArgs& a, int s0, int s1, int* next) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  const int per = ((s1 - s0 + nw - 1) / nw + 63) / 64 * 64;
+  const int b = s0 + wave * per, e = min(b + per, s1);
+  for (int s = b + lane; s < e; s += 64) {
+    const int x = a.experts[s];
+    if (x >= 0 && x < a.E) atomicAdd(next + wave * a.E + x, 1);
+  }
+}
+
+// offset[e] = sum of count[0 .. e) for e <= E, by the first wave.
+__device__ __forceinline__ void route_scan(const int* count, int* offset, int E) {
+  const int lane = threadIdx.x;
+  if (lane >= 64) return;
+  int before = 0;
+  for (int c = 0; c < E; c += 64) {
+    const int n = c + lane < E ? count[c + lane] : 0;
+    const int incl = wave_scan(n);
+    if (c + lane < E) offset[c + lane] = before + incl - n;
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  if (lane == 0) offset[E] = before;
+}
+
+// Turns counts per wave into places: expert x of wave w starts at base[x] plus
+// what earlier waves hold.
+__device__ __forceinline__ void route_bases(int* next, const int* base, int E) {
+  const int nw = blockDim.x >> 6;
+  for (int x = threadIdx.x; x < E; x += blockDim.x) {
+    int at = base[x];
+    for (int w = 0; w < nw; ++w) {
+      const int n = next[w * E + x];
+      next[w * E + x] = at;
+      at += n;
+    }
+  }
+}
+
+// ---- one workgroup does everything -------------------------------------------------
+// Slots it wrote itself are read back behind a barrier of the workgroup, which
+// orders them.
+constexpr int kSmallThreads = 512;
+template <typename In, int G, int C>
+__global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a) {
+  __shared__ __attribute__((aligned(16))) int next[kSmallThreads / 64 * G * C];
+  __shared__ __attribute__((aligned(16))) int hist[G * C];
+  __shared__ __attribute__((aligned(16))) int offset[G * C + 1];
+  const int nw = kSmallThreads / 64, n = a.T * a.k;
+  for (int i = threadIdx.x; i < nw * a.E; i += blockDim.x) next[i] = 0;
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
+  __syncthreads();
+  route_tokens<In, G, C>(a, 0, a.T, hist);
+  __syncthreads();
+  route_count(a, 0, n, next);
+  route_scan(hist, offset, a.E);
+  __syncthreads();
+  route_bases(next, offset, a.E);
+  for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = offset[i];
+  __syncthreads();
+  route_place(a, 0, n, offset[a.E], next);
+}
+
+// ---- many tokens: choose and count, then place ---------------------------------------
+constexpr int kRouteThreads = 256;
+template <typename In, int G, int C>
+__global__ __launch_bounds__(kRouteThreads) void route_select_kernel(RouteArgs a) {
+  __shared__ __attribute__((aligned(16))) int hist[G * C];
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
+  __syncthreads();
+  const int t0 = blockIdx.x * a.tokens;
+  route_tokens<In, G, C>(a, t0, min(t0 + a.tokens, a.T), hist);
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) a.counts[(size_t)blockIdx.x * a.E + i] = hist[i];
+}
+
+template <int EMAX>
+__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a) {
+  constexpr int NW = kRouteThreads / 64;
+  __shared__ __attribute__((aligned(16))) int next[NW * EMAX];
+  __shared__ __attribute__((aligned(16))) int count[EMAX];
+  __shared__ __attribute__((aligned(16))) int base[EMAX];
+  __shared__ __attribute__((aligned(16))) int offset[EMAX + 1];
+  const int nb = gridDim.x, me = blockIdx.x;
+  for (int i = threadIdx.x; i < NW * a.E; i += blockDim.x) next[i] = 0;
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) count[i] = base[i] = 0;
+  __syncthreads();
+  // every workgroup adds up the counts of all, and of those before it; the
+  // threads share the workgroups' rows, integer sums in any order
+  const int parts = a.E < kRouteThreads ? kRouteThreads / a.E : 1;
+  for (int i = threadIdx.x; i < parts * a.E; i += blockDim.x) {
+    const int x = i % a.E;
+    int all = 0, mine = 0;
+    for (int b = i / a.E; b < nb; b += parts) {
+      const int n = a.counts[(size_t)b * a.E + x];
+      all += n;
+      if (b < me) mine += n;
+    }
+    atomicAdd(count + x, all);
+    atomicAdd(base + x, mine);
+  }
+  const int s0 = me * a.tokens * a.k, s1 = min(s0 + a.tokens * a.k, a.T * a.k);
+  route_count(a, s0, s1, next);
+  __syncthreads();
+  route_scan(count, offset, a.E);
+  __syncthreads();
+  for (int x = threadIdx.x; x < a.E; x += blockDim.x) base[x] += offset[x];
+  __syncthreads();
+  route_bases(next, base, a.E);
+  if (me == 0)
+    for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = offset[i];
+  __syncthreads();
+  route_place(a, s0, s1, offset[a.E], next);
+}
+
+// ---- launches ---------------------------------------------------------------------------
+// Slots that one workgroup still takes by itself: below this a second launch
+// costs more than the others' help gives.
+constexpr long long kRouteSmall = 512;
+
+static int route_blocks(long long T, long long* tokens) {
+  // about one workgroup a CU, at least 16 tokens each (one pass of its lanes)
+  long long per = (T + 255) / 256;
+  per = (per + 15) / 16 * 16;
+  *tokens = per;
+  return (int)((T + per - 1) / per);
+}
+long long route_workspace_bytes(long long T, long long E, long long k) {
+  if (T * k <= kRouteSmall) return 0;
+  long long tokens;
+  return (long long)route_blocks(T, &tokens) * E * 4;
+}
+
+template <typename In, int G, int C>
+static hipError_t launch_route_as(RouteArgs a, hipStream_t stream) {
+  if ((long long)a.T * a.k <= kRouteSmall)
+    return launch_op(route_small_kernel<In, G, C>, dim3(1), dim3(kSmallThreads), stream, a);
+  long long tokens;
+  const int blocks = route_blocks(a.T, &tokens);
+  a.tokens = (int)tokens;
+  const hipError_t e =
+      launch_op(route_select_kernel<In, G, C>, dim3(blocks), dim3(kRouteThreads), stream, a);
+  if (e != hipSuccess) return e;
+  return launch_op(route_place_kernel<G * C>, dim3(blocks), dim3(kRouteThreads), stream, a);
+}
+template <typename In>
+static hipError_t launch_route_in(const RouteArgs& a, hipStream_t stream) {
+  // lanes a token: the fewest that hold E logits at 8 a lane, and k choices
+  if (a.E <= 128 && a.k <= 16) return launch_route_as<In, 16, 8>(a, stream);
+  if (a.E <= 256 && a.k <= 32) return launch_route_as<In, 32, 8>(a, stream);
+  if (a.E <= 512) return launch_route_as<In, 64, 8>(a, stream);
+  return launch_route_as<In, 64, 16>(a, stream);
+}
+
+hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* experts,
+                        int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
+                        bool renorm, hipStream_t stream) {
+  const int row = E * (f32 ? 4 : 2);
+  const int vec = ((uintptr_t)logits % 16 == 0 && row % 16 == 0) ? 1 : 0;
+  const RouteArgs a{logits, weights, experts, offsets, rows, (int32_t*)ws, T, E, k, renorm, vec, 0};
+  return f32 ? launch_route_in<float>(a, stream) : launch_route_in<uint16_t>(a, stream);
+}
+
+}  // namespace swiglu

@@ -465,6 +465,128 @@ swiglu_status_t swiglu_pack_kmajor(swiglu_handle_t h, const void* W1, const void
 swiglu_status_t swiglu_query_fp8(swiglu_handle_t h, int64_t M, int64_t N, int64_t K,
                                  swiglu_variant_t variant, swiglu_tile_t* tile);
 
+/* ---- mixture of experts ------------------------------------------------------
+ * A gated MLP whose weights are chosen per token: swiglu_route picks k of E
+ * experts a token and sorts the T k slots by expert, swiglu_grouped_forward
+ * computes the gated products of the sorted rows, swiglu_grouped_matmul the
+ * down products back into slot order, swiglu_combine_norm sums each token's
+ * slots and closes the block.  Slot t k + i is choice i of token t. */
+
+typedef enum {
+  SWIGLU_DTYPE_BF16 = 0,
+  SWIGLU_DTYPE_F32 = 1
+} swiglu_dtype_t;
+
+/* Bytes of swiglu_route's workspace (0: none needed; 0 also for sizes out of
+ * range).  It need not be cleared and holds nothing between calls; calls that
+ * may run at the same time need workspaces of their own. */
+int64_t swiglu_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
+
+/* For each of T tokens the k largest of its E logits (logits [T, E], bf16 or
+ * fp32 by dtype), the lower index first among equals:
+ *   experts [T, k]  int32, in falling order of the logits
+ *   weights [T, k]  fp32, exp(x - m) / S with m the token's largest logit and S
+ *                   the sum of exp(x - m) over the chosen experts (renormalize
+ *                   != 0) or over all E
+ *   rows [T k]      int32, the slots sorted by (expert, slot)
+ *   offsets [E + 1] int32, expert e's slots are rows[offsets[e]] up to
+ *                   rows[offsets[e + 1] - 1]
+ * A logit of -inf or NaN is masked off and never chosen; a token with fewer
+ * than k open logits has expert -1 and weight 0 in the places left over, which
+ * appear in no span; rows past offsets[E] are -1.  Where the largest logit is
+ * +inf the infinite ones share the weight.  T = 0 writes the offsets.
+ * The result does not depend on timing.  Limits: E <= 1024, k <= min(E, 64),
+ * T k < 2^31 (else UNSUPPORTED; k > E: INVALID_ARG).  INVALID_ARG also for a
+ * workspace too small and for overlapping tensors; pointers must be aligned to
+ * their elements (else UNSUPPORTED). */
+swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weights,
+                             int32_t* experts, int32_t* offsets, int32_t* rows, void* workspace,
+                             int64_t workspace_bytes, int64_t T, int64_t E, int64_t k,
+                             int32_t renormalize, swiglu_dtype_t dtype, hipStream_t stream);
+
+/* Y[i] = SiLU(a G_e) * (a U_e) for the sorted rows i in [offsets[e],
+ * offsets[e + 1]), with a = A[rows[i] / k], A [T, K], W [E, K, 2N] holding G_e
+ * in the even and U_e in the odd columns of expert e (the W_fused order), Y
+ * [R, N] in sorted order.  Rows of Y in no span are not written; a slot that
+ * names no row of A gives the products of a row of zeros.  Spans are held to
+ * [0, R] whatever offsets holds.  bf16 tensors, fp32 sums, one rounding.
+ * N % 8 == 0, K % 8 == 0, 16-byte aligned tensors, A and one expert's weights
+ * under 2 GiB, E <= 1024 (else UNSUPPORTED); all of W and Y may be larger.
+ * variant < 0: the kernel is chosen from R / E; 0 ... 4 force one (tests and
+ * tuning), another is INVALID_ARG. */
+swiglu_status_t swiglu_grouped_forward(swiglu_handle_t h, const void* A, const int32_t* rows,
+                                       const int32_t* offsets, const void* W, void* Y, int64_t T,
+                                       int64_t R, int64_t N, int64_t K, int64_t E, int64_t k,
+                                       int32_t variant, hipStream_t stream);
+
+/* Y[rows[i]] = A[i] W_e for the sorted rows of each expert e: A [R, K] in sorted
+ * order, W [E, K, N], Y [R, N] in slot order.  A slot outside [0, R) is not
+ * written; a slot must not appear twice.  Limits as swiglu_grouped_forward. */
+swiglu_status_t swiglu_grouped_matmul(swiglu_handle_t h, const void* A, const int32_t* rows,
+                                      const int32_t* offsets, const void* W, void* Y, int64_t R,
+                                      int64_t N, int64_t K, int64_t E, int32_t variant,
+                                      hipStream_t stream);
+
+/* The end of a block for T tokens of width D:
+ *   o = sum_j weights[t, j] B[t k + j] + S[t]       S [T, D] or NULL
+ *   o = o / sqrt(mean(o^2) + eps) * post            post [D] or NULL
+ *   o = o * gate                                    gate NULL, [D] (gate_ld 0)
+ *                                                   or [T, gate_ld >= D]
+ *   X_out = X + scale o
+ *   H = X_out / sqrt(mean(X_out^2) + eps) * pre     (X_out before its rounding)
+ * A row of B whose expert is negative takes no part, whatever it holds.
+ * B [T k, D], S, post, gate, pre and H are bf16, X and X_out of dtype, weights
+ * fp32 and experts int32 [T, k]; arithmetic is fp32.  k = 0 leaves the sum to
+ * S.  X_out may be X itself, else no output may overlap an input or the other
+ * (INVALID_ARG).  D % 8 == 0, D <= 16384, gate_ld % 8 == 0 and 16-byte aligned
+ * tensors (else UNSUPPORTED). */
+swiglu_status_t swiglu_combine_norm(swiglu_handle_t h, const void* B, const float* weights,
+                                    const int32_t* experts, const void* S, const void* X,
+                                    const void* post, const void* gate, const void* pre,
+                                    void* X_out, void* H, int64_t T, int64_t D, int64_t k,
+                                    float scale, float eps, int64_t gate_ld, swiglu_dtype_t dtype,
+                                    hipStream_t stream);
+
+/* ---- MXFP4 ---------------------------------------------------------------------
+ * The OCP Microscaling format with E2M1 elements: 32 consecutive k of a row
+ * share one E8M0 byte e; a 4-bit code (sign, 2 exponent bits, 1 mantissa bit)
+ * stands for 2^(e - 127) times one of +-{0, .5, 1, 1.5, 2, 3, 4, 6}; e = 255 is
+ * NaN.  Activations [rows, K] and weights [2N, K] (row 2n Gate column n, row
+ * 2n + 1 Up column n, see swiglu_pack_kmajor) are stored alike, in the order
+ * the matrix instructions read them.  With G = ceil(K / 256):
+ *   Q[(((rb G + g) 4 + s) 2 + h) 512 + 16 i + b]  holds the codes of row 32 rb + i
+ *       at k = 256 g + 64 s + 32 h + 2 b (low nibble) and the next (high nibble)
+ *   S[((rb G + g) 2 + h) 128 + 4 i + s]  its block's E8M0 byte
+ * for i < 32, s < 4, h < 2, b < 16; rows and k past the tensor hold code 0 at
+ * byte 127 (swiglu_quantize_mxfp4 writes them, and the forward relies on it). */
+
+/* Bytes of Q and of S for [rows, K] (0 when a size is <= 0 or out of range). */
+int64_t swiglu_mxfp4_bytes(int64_t rows, int64_t K);
+int64_t swiglu_mxfp4_scale_bytes(int64_t rows, int64_t K);
+
+/* MXFP4 of bf16 X [rows, K], padding included.  Per block: shared exponent
+ * floor(log2 max |x|) - 2 held to [-127, 127] (zeros and subnormals: -127; an
+ * infinity counts as 2^128), elements x 2^-shared to the nearest value, the
+ * even code at a tie, saturating at 6, the sign of zero kept.  A block with a
+ * NaN gets byte 255 and unspecified codes.  K % 32 == 0 and 16-byte aligned
+ * tensors (else UNSUPPORTED); outputs must not overlap X or each other. */
+swiglu_status_t swiglu_quantize_mxfp4(swiglu_handle_t h, const void* X, void* Q, void* S,
+                                      int64_t rows, int64_t K, hipStream_t stream);
+
+/* bf16 X [rows, K] from its codes, exact but for magnitudes from 2^128 on,
+ * which become infinities; NaN where the block's byte is 255. */
+swiglu_status_t swiglu_dequantize_mxfp4(swiglu_handle_t h, const void* Q, const void* S, void* X,
+                                        int64_t rows, int64_t K, hipStream_t stream);
+
+/* Y = bf16(SiLU(g) * u), g and u the Gate and Up products of activations
+ * (Q, SQ) [M, K] and weights (W, SW) [2N, K] in MXFP4; exact products, fp32
+ * sums.  N % 8 == 0, K % 32 == 0, 16-byte aligned tensors, the codes of each
+ * under 2 GiB (else UNSUPPORTED); Y [M, N] must not overlap an input.
+ * variant < 0: chosen from M and N; 0 ... 4 force one (tests and tuning). */
+swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const void* SQ,
+                                     const void* W, const void* SW, void* Y, int64_t M, int64_t N,
+                                     int64_t K, int32_t variant, hipStream_t stream);
+
 /* Number of compiled kernel configurations and their descriptions. */
 int32_t swiglu_config_count(void);
 swiglu_status_t swiglu_config_info(int32_t config_id, swiglu_tile_t* out);
