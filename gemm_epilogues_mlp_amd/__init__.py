@@ -159,8 +159,10 @@ def _ptr(x) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
+        # torch's current stream as a plain handle: torch.cuda.current_stream()
+        # builds a Stream object first, 2.9 of a small call's 6.5 us
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

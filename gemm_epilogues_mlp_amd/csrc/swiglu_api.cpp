@@ -32,6 +32,7 @@ struct swiglu_ctx {
 
 namespace swiglu {
 int handle_device(const ::swiglu_ctx* h) { return h->device; }
+int handle_cu_count(const ::swiglu_ctx* h) { return h->cu_count; }
 }  // namespace swiglu
 
 // ---- fixed device scratch for callers that cannot allocate -------------------

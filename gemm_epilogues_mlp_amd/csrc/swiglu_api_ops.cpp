@@ -130,7 +130,8 @@ swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const voi
                                      int64_t K, int32_t variant, hipStream_t stream) {
   if (!h || variant >= kFp4Variants) return SWIGLU_ERR_INVALID_ARG;
   const Fp4Call call{(const uint8_t*)Q, (const uint8_t*)SQ, (const uint8_t*)W, (const uint8_t*)SW,
-                     (uint16_t*)Y,      M,                  N,                 K};
+                     (uint16_t*)Y,      M,                  N,                 K,
+                     handle_cu_count(h)};
   bool noop;
   const int c = checks::forward_mxfp4(call, &noop);
   if (c != checks::kOk || noop) return (swiglu_status_t)c;

@@ -59,8 +59,9 @@ inline int route(const void* logits, const void* weights, const void* experts, c
       mul(T, E) > kMaxTotal)
     return kUnsupported;
   const unsigned size = dtype ? 4 : 2;
-  for (const void* p : {weights, experts, offsets, rows, ws})
+  for (const void* p : {weights, experts, offsets, rows})
     if (!aligned(p, 4)) return kUnsupported;
+  if (!aligned(ws, 16)) return kUnsupported;
   if (!aligned(logits, size)) return kUnsupported;
   const long long need = route_workspace_bytes(T, E, k);
   if (need > 0 && (!ws || ws_bytes < need)) return kInvalid;
@@ -148,6 +149,9 @@ inline int convert_mxfp4(const void* X, const void* Q, const void* S, long long 
   return kOk;
 }
 
+// 8 blocks of 32 rows past a tile's first stay within 32-bit offsets
+constexpr long long kMaxFp4K = 1LL << 22;
+
 inline int forward_mxfp4(const Fp4Call& c, bool* noop) {
   *noop = false;
   if (c.M < 0 || c.N < 0 || c.K < 0) return kInvalid;
@@ -156,7 +160,7 @@ inline int forward_mxfp4(const Fp4Call& c, bool* noop) {
     return kOk;
   }
   if (!c.Y || (c.K > 0 && (!c.A || !c.SA || !c.W || !c.SW))) return kInvalid;
-  if (c.M > kMaxInt - 256 || c.K > kMaxInt - 256 || c.N > (kMaxInt >> 1) - 256 || c.N % 8 != 0 ||
+  if (c.M > kMaxInt - 256 || c.K > kMaxFp4K || c.N > (kMaxInt >> 1) - 256 || c.N % 8 != 0 ||
       c.K % 32 != 0)
     return kUnsupported;
   if (!aligned16({c.Y, c.A, c.SA, c.W, c.SW})) return kUnsupported;

@@ -64,9 +64,7 @@ __global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint16_t* __res
     const int e = max((int)(m >> 7) - 2, 0);  // biased: floor(log2) + 127 - 2
     const uint32_t byte = pad ? 127u : (m > 0x7f80u ? 255u : (uint32_t)e);
     scales |= byte << (8 * s);
-    // 2^(e - 127) as fp32; e = 0 is a subnormal there
-    const float scale = __builtin_bit_cast(float, e > 0 ? (uint32_t)e << 23 : 1u << 22);
-    const uint32_t codes = e2m1_codes(v[s], scale);
+    const uint32_t codes = e2m1_codes(v[s], e8m0_scale(e));
     *reinterpret_cast<uint32_t*>(Q + ((((size_t)rg * 4 + s) * 2 + h) * 512 + 16 * i + 4 * q)) = codes;
   }
   if (q == 0) *reinterpret_cast<uint32_t*>(S + (((size_t)rg * 2 + h) * 128 + 4 * i)) = scales;
@@ -88,258 +86,275 @@ __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint8_t* __re
   const int row = 32 * rb + i;
   if (row >= rows) return;
   const uint32_t scales = *reinterpret_cast<const uint32_t*>(S + (((size_t)rg * 2 + h) * 128 + 4 * i));
+  uint32_t c[4];  // a group is stored whole, so all four loads are in bounds
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    c[s] = *reinterpret_cast<const uint32_t*>(Q + ((((size_t)rg * 4 + s) * 2 + h) * 512 + 16 * i + 4 * q));
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int k = 256 * g + 64 * s + 32 * h;
     if (k >= K) break;
-    const uint32_t c =
-        *reinterpret_cast<const uint32_t*>(Q + ((((size_t)rg * 4 + s) * 2 + h) * 512 + 16 * i + 4 * q));
     const int e = (int)((scales >> (8 * s)) & 0xffu);
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      f[j] = e == 255 ? __builtin_nanf("") : __builtin_ldexpf(e2m1_value(c >> (4 * j)), e - 127);
-    *reinterpret_cast<u32x4*>(X + (size_t)row * K + k + 8 * q) =
-        u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-              pack_bf16x2(f[6], f[7])};
+    const u32x4 v = e == 255 ? u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u}
+                             : e2m1_values(c[s], e8m0_scale(e));
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(X + (size_t)row * K + k + 8 * q));
   }
 }
 
 // ============================================================================
 // The product, LDS-tiled
 // ============================================================================
-// One workgroup: BM rows of A against BNW rows of W (Gate and Up rows
-// alternate, so a pair is two adjacent registers of a lane), as D = W A^T on
+// A tile is BM rows of A against BNW rows of W (Gate and Up rows alternate, so
+// a pair is two adjacent registers of a lane), as D = W A^T on
 // v_mfma_scale_f32_32x32x64_f8f6f4, which multiplies 4-bit sources at four
-// times the bf16 rate and applies the block scales itself.  A stage is 128 k:
-// 2 KB of every block of 32 rows, contiguous in HBM and copied as it is into a
-// ring of STAGES LDS stages; a fragment is one 16-byte read a lane at 16 x
-// lane, without bank conflicts and with no address arithmetic.  The scales of
-// a group of 256 k (two stages) come with its first stage into a ring of
-// their own.
-template <int BM, int BNW, int STAGES, int WGM, int WGN>
+// times the bf16 rate and applies the block scales itself.  K runs in stored
+// groups of 256 as two stages of 128 k each: 2 KB of every block of 32 rows,
+// contiguous in HBM and copied as it is into a ring of two groups in LDS; a
+// fragment is one 16-byte read a lane at 16 x lane, without bank conflicts.
+// The scales of a group come with its first stage.
+//
+// At this rate a tile's products are over in about 20 us, so what a tile costs
+// beside them shows: one workgroup stays on a CU and walks over tiles, the
+// ring running on from one to the next (a tile's last stages already load the
+// next one's first), and the output goes to memory straight from registers
+// (two lane exchanges give each lane 8 columns of a row), so that LDS stays
+// the ring's.
+template <int BM, int BNW, int WGM, int WGN>
 struct F4Tile {
   static constexpr int kWaves = WGM * WGN, kThreads = 64 * kWaves;
   static constexpr int BNY = BNW / 2;
   static constexpr int FA = BM / WGM / 32, FW = BNW / WGN / 32;  // blocks of 32 a wave
   static_assert(FA >= 1 && FW >= 1 && FA * WGM * 32 == BM && FW * WGN * 32 == BNW, "wave tile");
   static constexpr int NA = BM / 32, NW = BNW / 32, NB = NA + NW;  // blocks of 32 of the tile
-  static constexpr int STAGE_BYTES = NB * 2048;
-  static_assert(2 * NB % kWaves == 0, "every wave loads as much");
-  static constexpr int LOADS = 2 * NB / kWaves;  // 1 KB loads of a wave and stage
-  static constexpr int A_LOADS = 2 * NA / kWaves;
-  static_assert(2 * NA % kWaves == 0 && NA % 4 == 0, "a load is of one tensor");
-  static constexpr int SC_SLOT = NB * 256;       // scale bytes of a group
+  static constexpr int STAGE = NB * 2048, GROUP = 2 * STAGE;       // bytes
+  static constexpr int A_LOADS = 2 * NA / kWaves, LOADS = 2 * NB / kWaves;  // 1 KB loads of a wave
+  static_assert(2 * NA % kWaves == 0 && 2 * NB % kWaves == 0 && NA % 4 == 0 && NW % 4 == 0,
+                "every wave loads as much, a load is of one tensor");
+  static constexpr int SC_SLOT = NB * 256;  // scale bytes of a group
   static constexpr int SC_LOADS = (SC_SLOT / 1024 + kWaves - 1) / kWaves;
-  static_assert(SC_SLOT % 1024 == 0, "whole loads of scales");
-  static_assert(STAGES % 2 == 0 && STAGES >= 4, "whole groups of two stages");
-  // scale slots: a group's dwords are in registers before its first product, so
-  // its slot is free for the group that the ring brings next
-  static constexpr int GROUPS = STAGES / 2;
-  static constexpr int SC_OFF = STAGES * STAGE_BYTES;
-  static constexpr int JUNK = SC_OFF + GROUPS * SC_SLOT;  // for waves without scales to load
-  static constexpr int YLD = BNY + 8;
-  static constexpr int Y_BYTES = BM * YLD * 2;
-  static constexpr int RING_END = JUNK + 1024;
-  static constexpr int LDS_BYTES = RING_END > Y_BYTES ? RING_END : Y_BYTES;
+  static constexpr int SC_OFF = 2 * GROUP;
+  static constexpr int JUNK = SC_OFF + 2 * SC_SLOT;  // for waves without scales to load
+  static constexpr int LDS_BYTES = JUNK + 1024;
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
-  // loads of a stage: the first of a group brings the group's scales
-  __host__ __device__ static constexpr int loads(int pos) { return LOADS + (pos % 2 == 0 ? SC_LOADS : 0); }
-  // still in flight when the stage after position `pos` has to have landed,
-  // with the stages up to pos + STAGES - 1 issued
-  __host__ __device__ static constexpr int in_flight(int pos) {
-    int n = 0;
-    for (int d = 2; d < STAGES; ++d) n += loads(pos + d);
-    return n;
-  }
-  static_assert((STAGES - 1) * (LOADS + SC_LOADS) <= 63, "vmcnt range");
+  static_assert((GROUP & (GROUP - 1)) == 0, "the ring's two halves differ in one address bit");
+  // loads that may be in flight when the stage after this one has to have
+  // landed: those of the two stages behind it, one of which has scales
+  static constexpr int IN_FLIGHT = 2 * LOADS + SC_LOADS;
 };
 
-template <int BM, int BNW, int STAGES, int WGM, int WGN>
+template <int BM, int BNW, int WGM, int WGN>
 __global__ __launch_bounds__(64 * WGM * WGN) void fp4_tile_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ W,
     const uint8_t* __restrict__ SW, uint16_t* __restrict__ Y, int M, int N, int K, int group_m) {
-  using C = F4Tile<BM, BNW, STAGES, WGM, WGN>;
+  using C = F4Tile<BM, BNW, WGM, WGN>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wave_u = __builtin_amdgcn_readfirstlane(wave);
+  const int lane = threadIdx.x & 63;
+  const int wave_u = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wm = wave_u / WGN, wn = wave_u % WGN;
-  const int ntm = (M + BM - 1) / BM, ntn = (N + C::BNY - 1) / C::BNY;
-  // bands of group_m tile rows, column after column, contiguous on an XCD
-  const int t = xcd_remap(blockIdx.x, gridDim.x);
-  const int band = t / (group_m * ntn), in = t % (group_m * ntn);
-  const int high = min(ntm - band * group_m, group_m);
-  const int tm = band * group_m + in % high, tn = in / high;
+  const int ntm = (M + BM - 1) / BM, ntn = (N + C::BNY - 1) / C::BNY, ntiles = ntm * ntn;
+  // workgroup b runs on XCD b % 8; each XCD owns a contiguous range of tiles,
+  // which its workgroups take in turn
+  const int wg = blockIdx.x, nwg = gridDim.x, x = wg % 8;
+  const int stride = nwg / 8 + (x < nwg % 8 ? 1 : 0);
+  const int lo = x * (ntiles / 8) + min(x, ntiles % 8);
+  const int end = lo + ntiles / 8 + (x < ntiles % 8 ? 1 : 0);
+  const int first = lo + wg / 8;
+  if (first >= end) return;
 
   const int G = (K + 255) / 256;   // groups stored
-  const int nk = (K + 127) / 128;  // stages
+  const int Gp = max(G, 2);        // groups run: a ring of them at least
   const int nra = (M + 31) / 32, nrw = (2 * N + 31) / 32;
   const i32x4 rsA = make_rsrc(A, (uint32_t)nra * (uint32_t)G * 4096u);
   const i32x4 rsW = make_rsrc(W, (uint32_t)nrw * (uint32_t)G * 4096u);
-  const i32x4 rsSA = make_rsrc(SA, (uint32_t)nra * (uint32_t)G * 256u);
-  const i32x4 rsSW = make_rsrc(SW, (uint32_t)nrw * (uint32_t)G * 256u);
   const uint32_t lds0 = lds_addr(smem);
 
-  // Load q of stage `it` into ring position ST: 1 KB (half a stage of one
-  // block of 32 rows), A's blocks before W's.  Blocks past a tensor lie past
-  // its buffer and give zeros; stages past K are loaded but never multiplied.
+  // A tile's position: bands of group_m tile rows, column after column.
+  struct Tile {
+    int tm, tn;
+    uint32_t a, w;  // byte offsets of its first blocks' codes (a 16th for scales)
+  };
+  auto locate = [&](int t) __attribute__((always_inline)) {
+    Tile o{0, 0, kOutOfRange, kOutOfRange};  // past the last tile: zeros
+    if (t < end) {
+      const int band = t / (group_m * ntn), in = t % (group_m * ntn);
+      const int high = min(ntm - band * group_m, group_m);
+      o.tm = band * group_m + in % high;
+      o.tn = in / high;
+      o.a = (uint32_t)(o.tm * C::NA) * (uint32_t)G * 4096u;
+      o.w = (uint32_t)(o.tn * C::NW) * (uint32_t)G * 4096u;
+    }
+    o.tm = __builtin_amdgcn_readfirstlane(o.tm);
+    o.tn = __builtin_amdgcn_readfirstlane(o.tn);
+    o.a = __builtin_amdgcn_readfirstlane(o.a);
+    o.w = __builtin_amdgcn_readfirstlane(o.w);
+    return o;
+  };
+
+  // This wave's loads of a stage: load q is 1 KB, half a stage of one block of
+  // 32 rows, A's blocks before W's.  Blocks past a tensor lie past its buffer
+  // and give zeros.
   uint32_t off[C::LOADS];
 #pragma unroll
   for (int q = 0; q < C::LOADS; ++q) {
-    const int c = q * C::kWaves + wave_u, blk = c >> 1;
-    const int rb = q < C::A_LOADS ? tm * C::NA + blk : tn * C::NW + blk - C::NA;
-    off[q] = (uint32_t)rb * (uint32_t)G * 4096u + (uint32_t)(c & 1) * 1024u + (uint32_t)lane * 16u;
+    const int c = q * C::kWaves + wave_u, blk = q < C::A_LOADS ? c >> 1 : (c >> 1) - C::NA;
+    off[q] = (uint32_t)blk * (uint32_t)G * 4096u + (uint32_t)(c & 1) * 1024u + (uint32_t)lane * 16u;
   }
   // scales: load q is of four blocks of 32 rows, of one tensor
-  uint32_t sc_off[C::SC_LOADS], sc_dst[C::SC_LOADS];
+  uint32_t sc_off[C::SC_LOADS];
+  bool sc_a[C::SC_LOADS], sc_own[C::SC_LOADS];
   i32x4 rsS[C::SC_LOADS];
+  {
+    const i32x4 rsSA = make_rsrc(SA, (uint32_t)nra * (uint32_t)G * 256u);
+    const i32x4 rsSW = make_rsrc(SW, (uint32_t)nrw * (uint32_t)G * 256u);
 #pragma unroll
-  for (int q = 0; q < C::SC_LOADS; ++q) {
-    const int c = q * C::kWaves + wave_u, blk = 4 * c + (lane >> 4);
-    const bool a = 4 * c < C::NA, own = c * 1024 < C::SC_SLOT;
-    const int rb = a ? tm * C::NA + blk : tn * C::NW + blk - C::NA;
-    sc_off[q] = own ? (uint32_t)rb * (uint32_t)G * 256u + (uint32_t)(lane & 15) * 16u : kOutOfRange;
-    sc_dst[q] = own ? C::SC_OFF + c * 1024 : C::JUNK;
+    for (int q = 0; q < C::SC_LOADS; ++q) {
+      const int c = q * C::kWaves + wave_u, blk = 4 * c + (lane >> 4);
+      sc_a[q] = 4 * c < C::NA;
+      sc_own[q] = c * 1024 < C::SC_SLOT;
+      sc_off[q] = (uint32_t)(sc_a[q] ? blk : blk - C::NA) * (uint32_t)G * 256u + (uint32_t)(lane & 15) * 16u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rsS[q][i] = a ? rsSA[i] : rsSW[i];
+      for (int i = 0; i < 4; ++i) rsS[q][i] = sc_a[q] ? rsSA[i] : rsSW[i];
+    }
   }
-  auto dma = [&](int it, auto st_c, int q) __attribute__((always_inline)) {
-    constexpr int ST = decltype(st_c)::value;
+  // load q of stage HALF of group g of a tile into ring slot `slot`; groups
+  // past K load zeros
+  auto dma = [&](const Tile& o, int g, int slot, int half, int q) __attribute__((always_inline)) {
+    const bool in = g < G;
     if (q < C::LOADS) {
-      lds_dma16(lds0 + ST * C::STAGE_BYTES + (q * C::kWaves + wave_u) * 1024,
-                off[q] + (uint32_t)it * 2048u, q < C::A_LOADS ? rsA : rsW);
+      const uint32_t at = (q < C::A_LOADS ? o.a : o.w) + (uint32_t)g * 4096u + (uint32_t)half * 2048u;
+      lds_dma16(lds0 + slot * C::GROUP + half * C::STAGE + (q * C::kWaves + wave_u) * 1024,
+                off[q] + (in ? at : kOutOfRange), q < C::A_LOADS ? rsA : rsW);
     } else {
-      const int x = q - C::LOADS;
-      const uint32_t slot = sc_dst[x] == C::JUNK ? 0u : (uint32_t)((it >> 1) % C::GROUPS) * C::SC_SLOT;
-      lds_dma16(lds0 + sc_dst[x] + slot, sc_off[x] + (uint32_t)(it >> 1) * 256u, rsS[x]);
+      const int s = q - C::LOADS;
+      const uint32_t base = sc_a[s] ? o.a : o.w;
+      const bool there = in && sc_own[s] && base != kOutOfRange;
+      lds_dma16(lds0 + (sc_own[s] ? C::SC_OFF + slot * C::SC_SLOT + (s * C::kWaves + wave_u) * 1024
+                                  : C::JUNK),
+                sc_off[s] + (there ? base / 16u + (uint32_t)g * 256u : kOutOfRange), rsS[s]);
     }
   };
 
-  u32x4 af[2][C::FA], wf[2][C::FW];
-  uint32_t sa[2][C::FA], sw[2][C::FW];  // scale dwords of the group, by group parity
-  auto frag = [&](auto st_c, int sub, int r) __attribute__((always_inline)) {
-    constexpr int ST = decltype(st_c)::value;
-    const uint8_t* st = smem + ST * C::STAGE_BYTES + sub * 1024 + lane * 16;
+  u32x4 af[2][C::FA], wf[2][C::FW];              // fragments, by sub-step of 64 k
+  uint32_t sa[C::FA], sw[C::FW], sa_n[C::FA], sw_n[C::FW];  // a group's scale dwords; the next's
+  // where this wave's fragments are in the ring's current slot
+  uint32_t fa = (uint32_t)(wm * C::FA * 2048 + lane * 16);
+  uint32_t fw = (uint32_t)((C::NA + wn * C::FW) * 2048 + lane * 16);
+  auto frag = [&](uint32_t ba, uint32_t bw, int half, int sub, int r) __attribute__((always_inline)) {
+    const int at = half * C::STAGE + sub * 1024;
     if (r < C::FA)
-      af[sub][r] = *reinterpret_cast<const u32x4*>(st + (wm * C::FA + r) * 2048);
+      af[sub][r] = *reinterpret_cast<const u32x4*>(smem + ba + (at + r * 2048));
     else
-      wf[sub][r - C::FA] =
-          *reinterpret_cast<const u32x4*>(st + (C::NA + wn * C::FW + r - C::FA) * 2048);
+      wf[sub][r - C::FA] = *reinterpret_cast<const u32x4*>(smem + bw + (at + (r - C::FA) * 2048));
   };
   // lane i + 32 h: the dword at [block][h][i]
-  auto scales = [&](int group, int p) __attribute__((always_inline)) {
-    const uint8_t* s = smem + C::SC_OFF + group % C::GROUPS * C::SC_SLOT + lane * 4;
+  auto scales = [&](int slot) __attribute__((always_inline)) {
+    const uint8_t* s = smem + C::SC_OFF + slot * C::SC_SLOT + lane * 4;
 #pragma unroll
     for (int j = 0; j < C::FA; ++j)
-      sa[p][j] = *reinterpret_cast<const uint32_t*>(s + (wm * C::FA + j) * 256);
+      sa_n[j] = *reinterpret_cast<const uint32_t*>(s + (wm * C::FA + j) * 256);
 #pragma unroll
     for (int i = 0; i < C::FW; ++i)
-      sw[p][i] = *reinterpret_cast<const uint32_t*>(s + (C::NA + wn * C::FW + i) * 256);
+      sw_n[i] = *reinterpret_cast<const uint32_t*>(s + (C::NA + wn * C::FW + i) * 256);
   };
-
+  auto take_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < C::FA; ++j) sa[j] = sa_n[j];
+#pragma unroll
+    for (int i = 0; i < C::FW; ++i) sw[i] = sw_n[i];
+  };
   f32x16 acc[C::FW][C::FA];
-#pragma unroll
-  for (int i = 0; i < C::FW; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FA; ++j) acc[i][j] = f32x16{};
 
-  // Stage `it` at position POS of the unrolled loop (ring position POS %
-  // STAGES).  Sub-step 0 reads the fragments of sub-step 1; behind the barrier
-  // (the next stage has landed, every wave has read this one) sub-step 1 reads
-  // the next stage's first fragments and loads stage it + STAGES in this one's
-  // place.
+  // Sub-step B (64 k) of a group.  The even ones read the other sub-step of
+  // their stage; the odd ones wait for the next stage, and behind the barrier
+  // (every wave has read this stage) read the next one's first fragments and
+  // load the stage of the group after next in this one's place.
   constexpr int NMF = C::FW * C::FA, NFRAG = C::FW + C::FA;
-  auto kstep = [&](int it, auto pos_c) __attribute__((always_inline)) {
-    constexpr int POS = decltype(pos_c)::value;
-    constexpr int ST = POS % STAGES, GP = (POS / 2) & 1;
-    using Cur = std::integral_constant<int, ST>;
-    using Next = std::integral_constant<int, (ST + 1) % STAGES>;
-    auto half = [&](auto sub_c) __attribute__((always_inline)) {
-      constexpr int SUB = decltype(sub_c)::value;
-      constexpr int B = (POS % 2) * 2 + SUB;  // step of the group: the scale byte
+  auto step = [&](auto b_c, const Tile& o, int g, int slot) __attribute__((always_inline)) {
+    constexpr int B = decltype(b_c)::value, SUB = B & 1, HALF = B >> 1;
+    constexpr int TL = C::LOADS + (HALF == 0 ? C::SC_LOADS : 0);
+    if constexpr (SUB == 1) {
+      wait_vmcnt<C::IN_FLIGHT>();
+      __syncthreads();
+      if constexpr (HALF == 1) scales(slot ^ 1);
+    }
+    const uint32_t na = HALF == 1 && SUB == 1 ? fa ^ C::GROUP : fa;
+    const uint32_t nw = HALF == 1 && SUB == 1 ? fw ^ C::GROUP : fw;
+    auto one = [&](auto q_c) __attribute__((always_inline)) {
+      constexpr int Q = decltype(q_c)::value, i = Q / C::FA, j = Q % C::FA;
+      acc[i][j] = mfma32_f4<B, B>(wf[SUB][i], af[SUB][j], acc[i][j], sw[i], sa[j]);
+#pragma unroll
+      for (int r = Q * NFRAG / NMF; r < (Q + 1) * NFRAG / NMF; ++r)
+        frag(na, nw, SUB == 0 ? HALF : HALF ^ 1, SUB ^ 1, r);
       if constexpr (SUB == 1) {
-        wait_vmcnt<C::in_flight(POS)>();
-        __syncthreads();
-        if constexpr (POS % 2 == 1) scales((it + 1) >> 1, GP ^ 1);
+#pragma unroll
+        for (int q = Q * TL / NMF; q < (Q + 1) * TL / NMF; ++q) dma(o, g, slot, HALF, q);
       }
-      constexpr int TL = C::loads(POS + STAGES);
-      auto slot = [&](auto q_c) __attribute__((always_inline)) {
-        constexpr int Q = decltype(q_c)::value;
-        constexpr int i = Q / C::FA, j = Q % C::FA;
-        acc[i][j] = mfma32_f4<B, B>(wf[SUB][i], af[SUB][j], acc[i][j], sw[GP][i], sa[GP][j]);
-#pragma unroll
-        for (int x = Q * NFRAG / NMF; x < (Q + 1) * NFRAG / NMF; ++x) {
-          if constexpr (SUB == 0) frag(Cur{}, 1, x);
-          else frag(Next{}, 0, x);
-        }
-        if constexpr (SUB == 1) {
-#pragma unroll
-          for (int x = Q * TL / NMF; x < (Q + 1) * TL / NMF; ++x) dma(it + STAGES, Cur{}, x);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      [&]<int... Q>(std::integer_sequence<int, Q...>) __attribute__((always_inline)) {
-        (slot(std::integral_constant<int, Q>{}), ...);
-      }(std::make_integer_sequence<int, NMF>{});
+      __builtin_amdgcn_sched_barrier(0);
     };
-    half(std::integral_constant<int, 0>{});
-    half(std::integral_constant<int, 1>{});
+    [&]<int... Q>(std::integer_sequence<int, Q...>) __attribute__((always_inline)) {
+      (one(std::integral_constant<int, Q>{}), ...);
+    }(std::make_integer_sequence<int, NMF>{});
   };
 
-  // ---- prologue: all stages of the ring in flight, the first one's fragments ------
-  auto fill = [&](auto st_c) __attribute__((always_inline)) {
-    constexpr int S = decltype(st_c)::value;
+  // ---- the first tile's first two groups, and the fragments of its first stage -----
+  Tile cur = locate(first), nxt = cur;
 #pragma unroll
-    for (int q = 0; q < C::loads(S); ++q) dma(S, st_c, q);
-  };
-  [&]<int... S>(std::integer_sequence<int, S...>) __attribute__((always_inline)) {
-    (fill(std::integral_constant<int, S>{}), ...);
-  }(std::make_integer_sequence<int, STAGES>{});
-  wait_vmcnt<C::in_flight(2 * STAGES - 1) + C::loads(STAGES - 1)>();
+  for (int st = 0; st < 4; ++st) {
+#pragma unroll
+    for (int q = 0; q < C::LOADS + (st % 2 == 0 ? C::SC_LOADS : 0); ++q)
+      dma(cur, st / 2, st / 2, st % 2, q);
+  }
+  wait_vmcnt<3 * C::LOADS + C::SC_LOADS>();
   __syncthreads();
-  scales(0, 0);
+  scales(0);
 #pragma unroll
-  for (int r = 0; r < NFRAG; ++r) frag(std::integral_constant<int, 0>{}, 0, r);
+  for (int r = 0; r < NFRAG; ++r) frag(fa, fw, 0, 0, r);
 
-  // ---- main loop: unrolled over two rings of stages (the parity of the groups) -----
-  constexpr int UNR = STAGES % 4 == 0 ? STAGES : 2 * STAGES;
-  int it = 0;
-  for (; it + UNR <= nk; it += UNR)
-    [&]<int... S>(std::integer_sequence<int, S...>) __attribute__((always_inline)) {
-      (kstep(it + S, std::integral_constant<int, S>{}), ...);
-    }(std::make_integer_sequence<int, UNR>{});
-  [&]<int... S>(std::integer_sequence<int, S...>) __attribute__((always_inline)) {
-    ((it + S < nk ? (kstep(it + S, std::integral_constant<int, S>{}), 0) : 0), ...);
-  }(std::make_integer_sequence<int, UNR - 1>{});
-
-  // ---- epilogue: SiLU(Gate) Up, bf16 tile through LDS, 16-byte row stores ----------
-  wait_vmcnt<0>();
-  __syncthreads();
-  int etid = threadIdx.x;
-  asm volatile("" : "+v"(etid));
-  const int el = etid & 63;
-  uint16_t* ys = reinterpret_cast<uint16_t*>(smem);
+  int slot = 0;
+  for (int t = first; t < end; t += stride) {
+    nxt = locate(t + stride);
 #pragma unroll
-  for (int i = 0; i < C::FW; ++i)
+    for (int i = 0; i < C::FW; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FA; ++j) acc[i][j] = f32x16{};
+    for (int g = 0; g < Gp; ++g) {
+      take_scales();
+      const bool over = g + 2 >= Gp;  // the group to load is the next tile's
+      const Tile o{0, 0, over ? nxt.a : cur.a, over ? nxt.w : cur.w};
+      const int lg = over ? g + 2 - Gp : g + 2;
+      step(std::integral_constant<int, 0>{}, o, lg, slot);
+      step(std::integral_constant<int, 1>{}, o, lg, slot);
+      step(std::integral_constant<int, 2>{}, o, lg, slot);
+      step(std::integral_constant<int, 3>{}, o, lg, slot);
+      fa ^= C::GROUP;
+      fw ^= C::GROUP;
+      slot ^= 1;
+    }
+    // SiLU(Gate) Up of this tile.  Registers 4 q .. 4 q + 3 are W rows 8 q + 4 h
+    // + 0 .. 3 (h = lane / 32), i.e. output columns 4 q + 2 h and + 1; the
+    // exchanges leave columns 0 .. 7 of the block of 16 in the lower half of
+    // the wave, 8 .. 15 in the upper one.
 #pragma unroll
     for (int j = 0; j < C::FA; ++j) {
-      const f32x16& d = acc[i][j];
-      uint16_t* y = ys + ((wm * C::FA + j) * 32 + (el & 31)) * C::YLD +
-                    ((wn * C::FW + i) * 32 + 4 * (el >> 5)) / 2;
+      const int row = cur.tm * BM + (wm * C::FA + j) * 32 + (lane & 31);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)  // W rows + 8 q + 0 .. 3: Gate, Up, Gate, Up
-        *reinterpret_cast<uint32_t*>(y + 4 * q) =
-            pack_bf16x2(silu(d[4 * q]) * d[4 * q + 1], silu(d[4 * q + 2]) * d[4 * q + 3]);
+      for (int i = 0; i < C::FW; ++i) {
+        const f32x16& d = acc[i][j];
+        uint32_t p[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          p[q] = pack_bf16x2(silu(d[4 * q]) * d[4 * q + 1], silu(d[4 * q + 2]) * d[4 * q + 3]);
+        swap_halves(p[0], p[2]);
+        swap_halves(p[1], p[3]);
+        const int col = cur.tn * C::BNY + (wn * C::FW + i) * 16 + 8 * (lane >> 5);
+        if (row < M && col < N)
+          *reinterpret_cast<u32x4*>(Y + (size_t)row * N + col) = u32x4{p[0], p[2], p[1], p[3]};
+      }
     }
-  __syncthreads();
-  constexpr int YCH = C::BNY / 8;
-  for (int p = tid; p < BM * YCH; p += C::kThreads) {
-    const int row = p / YCH, cq = p % YCH;
-    const int gr = tm * BM + row, gc = tn * C::BNY + cq * 8;
-    if (gr < M && gc < N)
-      *reinterpret_cast<u32x4*>(Y + (size_t)gr * N + gc) =
-          *reinterpret_cast<const u32x4*>(ys + row * C::YLD + cq * 8);
+    cur = nxt;
   }
+  // the zero loads issued past the last tile still write LDS
+  wait_vmcnt<0>();
 }
 
 // ============================================================================
@@ -406,15 +421,16 @@ __global__ __launch_bounds__(64 * NW) void fp4_stream_kernel(
 // ============================================================================
 // Launches
 // ============================================================================
-template <int BM, int BNW, int STAGES, int WGM, int WGN>
+template <int BM, int BNW, int WGM, int WGN>
 static hipError_t launch_f4_tile(const Fp4Call& c, hipStream_t stream) {
-  using C = F4Tile<BM, BNW, STAGES, WGM, WGN>;
+  using C = F4Tile<BM, BNW, WGM, WGN>;
   const long long ntm = (c.M + BM - 1) / BM, ntn = (c.N + C::BNY - 1) / C::BNY;
   if (ntm * ntn > 0x7fffffffLL) return hipErrorInvalidValue;
   const int group_m = (int)std::min(ntm, 4LL);
-  return launch_op(fp4_tile_kernel<BM, BNW, STAGES, WGM, WGN>, dim3((unsigned)(ntm * ntn)),
-                   dim3(C::kThreads), stream, c.A, c.SA, c.W, c.SW, c.Y, (int)c.M, (int)c.N,
-                   (int)c.K, group_m);
+  const int per_cu = C::LDS_BYTES <= 80 * 1024 ? 2 : 1;
+  const long long wgs = std::min<long long>(ntm * ntn, (long long)c.cu_count * per_cu);
+  return launch_op(fp4_tile_kernel<BM, BNW, WGM, WGN>, dim3((unsigned)wgs), dim3(C::kThreads),
+                   stream, c.A, c.SA, c.W, c.SW, c.Y, (int)c.M, (int)c.N, (int)c.K, group_m);
 }
 template <int MT, int NW>
 static hipError_t launch_f4_stream(const Fp4Call& c, hipStream_t stream) {
@@ -439,8 +455,8 @@ hipError_t launch_forward_mxfp4(const Fp4Call& c, int variant, hipStream_t strea
     case 0: return launch_f4_stream<1, 4>(c, stream);
     case 1: return launch_f4_stream<2, 4>(c, stream);
     case 2: return launch_f4_stream<4, 4>(c, stream);
-    case 3: return launch_f4_tile<128, 128, 4, 2, 2>(c, stream);
-    default: return launch_f4_tile<256, 256, 4, 2, 4>(c, stream);
+    case 3: return launch_f4_tile<128, 128, 2, 2>(c, stream);
+    default: return launch_f4_tile<256, 256, 2, 4>(c, stream);
   }
 }
 

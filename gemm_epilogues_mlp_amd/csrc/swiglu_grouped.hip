@@ -68,13 +68,18 @@ struct GroupTile {
   static constexpr int ACH = BK / 8, WCH = BNW / 8;  // 16-byte chunks of a row
   static constexpr int A_BYTES = BM * BK * 2, W_BYTES = BK * BNW * 2;
   static constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
-  static constexpr int A_LOADS = BM * ACH / kThreads, W_LOADS = BK * WCH / kThreads;
-  static_assert(BM * ACH % kThreads == 0 && BK * WCH % kThreads == 0, "whole loads");
+  static constexpr int A_CHUNKS = BM * ACH;
+  static constexpr int A_LOADS = (A_CHUNKS + kThreads - 1) / kThreads, W_LOADS = BK * WCH / kThreads;
+  static_assert(A_CHUNKS % 64 == 0 && BK * WCH % kThreads == 0, "a wave's chunks are whole");
   static constexpr int LOADS = A_LOADS + W_LOADS;
   static constexpr int LH = LOADS / 2;
   static_assert(LH >= 1 && LOADS * (STAGES - 2) + LH <= 63, "vmcnt range");
   static constexpr int YLD = BNY + 8;  // padded row of the output staging tile
-  static constexpr int RING = STAGES * STAGE_BYTES;
+  // a wave without chunks of A in a load fetches zeros into a slot of its own,
+  // so that every wave has the same number of loads in flight
+  static constexpr bool NEED_JUNK = A_CHUNKS % kThreads != 0;
+  static constexpr int JUNK = STAGES * STAGE_BYTES;
+  static constexpr int RING = JUNK + (NEED_JUNK ? 1024 : 0);
   static constexpr int Y_BYTES = BM * YLD * 2;
   static constexpr int LDS_BYTES = RING > Y_BYTES ? RING : Y_BYTES;
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
@@ -97,7 +102,12 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
                                              int tn, uint8_t* smem) {
   using C = GroupTile<OP, BM, BNW, STAGES, WGM, WGN>;
   constexpr int BK = C::BK;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // a copy of the thread index that the compiler cannot see through: else it
+  // keeps the offsets of every tile height in registers around the loop over
+  // units, and spills
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, wave = tid >> 6;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
   const int wm = wave / WGN, wn = wave % WGN;
   const int K = g.K, ldw = g.ldw;
@@ -114,7 +124,7 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
   for (int i = 0; i < C::A_LOADS; ++i) {
     const int p = tid + C::kThreads * i;
     const int row = p / C::ACH, c = (p % C::ACH) ^ C::a_swz(row);
-    const int ar = row < nrows ? group_a_row<OP>(g, pos0 + row) : -1;
+    const int ar = row < min(nrows, BM) ? group_a_row<OP>(g, pos0 + row) : -1;
     a_off[i] = ar >= 0 ? ((uint32_t)ar * (uint32_t)K + c * 8) * 2u : 0u;
     a_k[i] = ar >= 0 ? c * 8 : 0x3fffffff;
   }
@@ -132,8 +142,10 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
     const int k0 = it < nk ? it * BK : K;
     const uint32_t sbase = lds0 + ST * C::STAGE_BYTES;
     if (q < C::A_LOADS) {
+      const int p0 = C::kThreads * q + 64 * wave_u;  // this wave's first chunk
+      const bool own = p0 < C::A_CHUNKS;
       const uint32_t off = k0 + a_k[q] < K ? a_off[q] + (uint32_t)k0 * 2u : kOutOfRange;
-      lds_dma16(sbase + (C::kThreads * q + 64 * wave_u) * 16, off, rsA);
+      lds_dma16(own ? sbase + p0 * 16 : lds0 + C::JUNK, off, rsA);
     } else {
       const int i = q - C::A_LOADS;
       lds_dma16(sbase + C::A_BYTES + (C::kThreads * i + 64 * wave_u) * 16,
@@ -277,33 +289,48 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
   }
 }
 
-// Units are ordered expert by expert, within one in bands of up to 8 row tiles,
-// column after column, so that the workgroups of an XCD share weight columns
-// and rows of A in its L2.  An expert's last tile runs at half the height when
-// its rows fit (half the matrix instructions); HWGM = 0: no such form.
-template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int HWGM, int HWGN>
+// Within an expert the tiles go in bands of up to 8 row tiles, column after
+// column, so that the workgroups of an XCD share weight columns and rows of A
+// in its L2.  Workgroup b runs on XCD b % 8 and takes units of that XCD's range
+// in turn: how many there are is known on the device only, and with short
+// tiles an eighth of the work may be more than an eighth of the units.  The
+// last tile of an expert runs at the height that its rows need (fewer matrix
+// instructions).
+template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN>
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupArgs g, int ntn) {
-  using C = GroupTile<OP, BM, BNW, STAGES, WGM, WGN>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
-  GroupUnit u;
-  if (!group_find<BM>(g.offsets, g.E, g.R, ntn, blockIdx.x, u)) return;
-  const int ntm = (u.rows + BM - 1) / BM;
-  constexpr int kBand = 8;
-  const int band = u.local / (kBand * ntn), in = u.local % (kBand * ntn);
-  const int high = min(ntm - band * kBand, kBand);
-  const int tm = band * kBand + in % high, tn = in / high;
-  const int nrows = u.rows - tm * BM;
-  if constexpr (HWGM > 0) {
-    using H = GroupTile<OP, BM / 2, BNW, STAGES, HWGM, HWGN>;
-    static_assert(C::kThreads == H::kThreads && H::LDS_BYTES <= C::LDS_BYTES, "one workgroup");
-    if (nrows <= BM / 2) {
-      grouped_tile<OP, BM / 2, BNW, STAGES, HWGM, HWGN>(g, u.expert, u.first + tm * BM, nrows, tn,
-                                                        smem);
-      return;
+  constexpr int P = BM / PARTS;  // rows of a part
+  constexpr int LDS = GroupTile<OP, BM, BNW, STAGES, WGM, WGN>::LDS_BYTES + (PARTS > 1 ? 1024 : 0);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
+  const GroupRange range = group_range<BM, PARTS>(g.offsets, g.E, g.R, ntn, blockIdx.x % 8);
+  const int nwg = ((int)gridDim.x + 7 - (int)(blockIdx.x % 8)) / 8;  // of this XCD
+  for (int t = range.begin + (int)blockIdx.x / 8; t < range.end; t += nwg) {
+    const GroupUnit u = group_unit<BM>(g.offsets, g.E, g.R, ntn, t);
+    const int ntm = (u.rows + BM - 1) / BM;
+    constexpr int kBand = 8;
+    const int band = u.local / (kBand * ntn), in = u.local % (kBand * ntn);
+    const int high = min(ntm - band * kBand, kBand);
+    const int tm = band * kBand + in % high, tn = in / high;
+    const int pos0 = u.first + tm * BM, left = u.rows - tm * BM;
+    const int parts = (min(left, BM) + P - 1) / P;
+    auto part = [&](auto n_c) __attribute__((always_inline)) {
+      constexpr int ROWS = decltype(n_c)::value * P;
+      // short tiles: the waves side by side where two rows of them do not fit
+      constexpr int WM = ROWS / 32 >= PWGM && ROWS % (32 * PWGM) == 0 ? PWGM : 1;
+      constexpr int WN = PWGM * PWGN / WM;
+      static_assert(GroupTile<OP, ROWS, BNW, STAGES, WM, WN>::LDS_BYTES <= LDS, "LDS");
+      grouped_tile<OP, ROWS, BNW, STAGES, WM, WN>(g, u.expert, pos0, left, tn, smem);
+    };
+    if (parts == PARTS) {
+      grouped_tile<OP, BM, BNW, STAGES, WGM, WGN>(g, u.expert, pos0, min(left, BM), tn, smem);
+    } else if (PARTS >= 4 && parts == 3) {
+      if constexpr (PARTS >= 4) part(std::integral_constant<int, 3>{});
+    } else if (PARTS >= 4 && parts == 2) {
+      if constexpr (PARTS >= 4) part(std::integral_constant<int, 2>{});
+    } else {
+      if constexpr (PARTS >= 2) part(std::integral_constant<int, 1>{});
     }
+    __syncthreads();  // the next unit's loads overwrite this one's rows of Y in LDS
   }
-  grouped_tile<OP, BM, BNW, STAGES, WGM, WGN>(g, u.expert, u.first + tm * BM, min(nrows, BM), tn,
-                                              smem);
 }
 
 // ============================================================================
@@ -319,8 +346,11 @@ template <int OP, int MT, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 2)))
 void grouped_stream_kernel(GroupArgs g, int nslab) {
   __shared__ __attribute__((aligned(16))) f32x4 red[NW * MT * 8 * 64];
-  GroupUnit u;
-  if (!group_find<16 * MT>(g.offsets, g.E, g.R, nslab, blockIdx.x, u)) return;
+  const int x = blockIdx.x % 8;
+  const GroupRange range = group_range<16 * MT, 1>(g.offsets, g.E, g.R, nslab, x);
+  const int t = range.begin + (int)blockIdx.x / 8;
+  if (t >= range.end) return;
+  const GroupUnit u = group_unit<16 * MT>(g.offsets, g.E, g.R, nslab, t);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int slab = u.local % nslab, pos0 = u.first + u.local / nslab * (16 * MT);
   const int nrows = min(u.first + u.rows - pos0, 16 * MT);
@@ -411,19 +441,26 @@ static long long max_row_tiles(long long R, long long E, long long bm) {
   return std::min(R, (R + some * (bm - 1)) / bm);
 }
 
-template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int HWGM, int HWGN>
+template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN>
 static hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
-  using C = GroupTile<OP, BM, BNW, STAGES, WGM, WGN>;
+  static_assert(WGM * WGN == PWGM * PWGN && (PARTS == 1 || PARTS == 2 || PARTS == 4), "one workgroup");
   const long long ntn = (g.ldw + BNW - 1) / BNW;
+  // Every XCD's range needs workgroups there.  With short tiles an eighth of
+  // the work can be up to 2.2 eighths of the units; while the launch is about
+  // a round of workgroups, the extra ones cost nothing and a second unit in
+  // turn would double the time, beyond that the loop takes what is left over.
   const long long units = max_row_tiles(g.R, g.E, BM) * ntn;
-  if (units > 0x7fffffffLL) return hipErrorInvalidValue;
-  return launch_op(grouped_tile_kernel<OP, BM, BNW, STAGES, WGM, WGN, HWGM, HWGN>,
-                   dim3((unsigned)units), dim3(C::kThreads), stream, g, (int)ntn);
+  const long long grid = (units * (PARTS > 1 && units < 1024 ? 2 : 1) + 7) / 8 * 8;
+  if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
+  return launch_op(grouped_tile_kernel<OP, BM, BNW, STAGES, WGM, WGN, PARTS, PWGM, PWGN>,
+                   dim3((unsigned)grid), dim3(64 * WGM * WGN), stream, g, (int)ntn);
 }
 template <int OP, int MT, int NW>
 static hipError_t launch_stream(const GroupArgs& g, hipStream_t stream) {
   const long long nslab = (g.ldw + 127) / 128;
-  const long long units = max_row_tiles(g.R, g.E, 16 * MT) * nslab;
+  // one workgroup a unit: all units weigh the same, so no XCD has more than an
+  // eighth of them, rounded up
+  const long long units = (max_row_tiles(g.R, g.E, 16 * MT) * nslab + 7) / 8 * 8;
   if (units > 0x7fffffffLL) return hipErrorInvalidValue;
   return launch_op(grouped_stream_kernel<OP, MT, NW>, dim3((unsigned)units), dim3(64 * NW),
                    stream, g, (int)nslab);
@@ -433,28 +470,32 @@ template <int OP>
 static hipError_t launch_grouped_op(const GroupArgs& g, int variant, hipStream_t stream) {
   switch (variant) {
     case 0: return launch_stream<OP, 1, 8>(g, stream);
-    case 1: return launch_stream<OP, 2, 8>(g, stream);
-    case 2: return launch_tile<OP, 64, 128, 4, 2, 2, 0, 0>(g, stream);
-    case 3: return launch_tile<OP, 128, 128, 4, 2, 2, 2, 2>(g, stream);
-    default: return launch_tile<OP, 256, 256, 4, 4, 2, 2, 4>(g, stream);
+    case 1: return launch_tile<OP, 64, 128, 4, 2, 2, 1, 2, 2>(g, stream);
+    case 2: return launch_tile<OP, 128, 128, 4, 2, 2, 2, 2, 2>(g, stream);
+    default: return launch_tile<OP, 256, 256, 4, 4, 2, 4, 2, 4>(g, stream);
   }
 }
 
-// Rows an expert on average decide; the counts themselves are on the device.
-static int grouped_variant(long long R, long long E) {
-  const long long mean = (R + E - 1) / E;
-  if (mean <= 8) return 0;
-  if (mean <= 24) return 1;
-  if (mean <= 64) return 2;
-  if (mean <= 160) return 3;
-  return 4;
+// The counts are on the device; the mean rows of an expert decide, and whether
+// there is a workgroup for every CU.  Measured (us, 2048 x 2816 weights, 32
+// experts, variants 0 / 1 / 3): mean 8: 61 / 70 / 75, 24: 114 / 72 / 78, 64: 244
+// / 93 / 80.  With few units the wide tiles stream better (8 experts, 3584 x
+// 4736, mean 8, 0 / 3: 57 / 52), and where even those leave CUs idle the
+// 128-row ones (8 experts, 2368 x 3584, mean 8, 0 / 2 / 3: 26.6 / 22.0 / 25.4).
+static int grouped_variant(long long R, long long E, long long ldw) {
+  const long long some = std::min(R, E), mean = (R + E - 1) / E;
+  const long long wide = some * ((mean + 255) / 256) * ((ldw + 255) / 256);
+  if (wide < 128) return 2;
+  if (wide >= 200 && mean <= 10) return 0;
+  if (wide >= 200 && mean <= 28) return 1;
+  return 3;
 }
 
 hipError_t launch_grouped(bool up, const uint16_t* A, const int32_t* rows, const int32_t* offsets,
                           const uint16_t* W, uint16_t* Y, int TA, int R, int N, int K, int E,
                           int k, int variant, hipStream_t stream) {
   const GroupArgs g{A, rows, offsets, W, Y, TA, R, N, K, E, k, up ? 2 * N : N};
-  if (variant < 0) variant = grouped_variant(R, E);
+  if (variant < 0) variant = grouped_variant(R, E, g.ldw);
   return up ? launch_grouped_op<GROUP_UP>(g, variant, stream)
             : launch_grouped_op<GROUP_DOWN>(g, variant, stream);
 }

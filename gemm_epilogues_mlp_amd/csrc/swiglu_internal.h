@@ -107,8 +107,9 @@ hipError_t launch_pack_frag(const uint16_t* W1, const uint16_t* W2, uint16_t* P,
 hipError_t launch_pack_kmajor(const uint16_t* W1, const uint16_t* W2, uint16_t* Wt, int N, int K,
                               hipStream_t stream, int cu_count);
 
-// Device of a handle (swiglu_api.cpp).
+// Device of a handle and its compute units (swiglu_api.cpp).
 int handle_device(const ::swiglu_ctx* h);
+int handle_cu_count(const ::swiglu_ctx* h);
 
 // ---- mixture-of-experts operators (swiglu_route.hip, swiglu_grouped.hip,
 // swiglu_norm.hip); sizes are checked by the caller -----------------------------
@@ -118,7 +119,7 @@ hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* e
                         int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
                         bool renorm, hipStream_t stream);
 // Grouped products; TA: rows of A, variant < 0: by rule
-constexpr int kGroupedVariants = 5;
+constexpr int kGroupedVariants = 4;
 hipError_t launch_grouped(bool up, const uint16_t* A, const int32_t* rows, const int32_t* offsets,
                           const uint16_t* W, uint16_t* Y, int TA, int R, int N, int K, int E,
                           int k, int variant, hipStream_t stream);
@@ -147,6 +148,7 @@ struct Fp4Call {
   const uint8_t *A, *SA, *W, *SW;
   uint16_t* Y;
   long long M, N, K;
+  int cu_count;
 };
 constexpr int kFp4Variants = 5;
 hipError_t launch_forward_mxfp4(const Fp4Call& c, int variant, hipStream_t stream);

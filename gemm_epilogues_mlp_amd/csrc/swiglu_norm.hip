@@ -83,6 +83,31 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void combine_norm_kernel(N
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[v][i] = 0.0f;
   }
+  // With one vector a lane everything else is loaded here, ahead of the sums
+  // that would make it wait; with more the registers go to rows of B.
+  constexpr bool kEarly = VPL == 1;
+  const uint16_t* none = a.pre;  // where an input is absent, any row that is there
+  u32x4 vs[VPL], vpost[VPL], vgate[VPL], vpre[VPL], vx[VPL], vx2[VPL];
+  auto load_s = [&](int v) __attribute__((always_inline)) {
+    vs[v] = a.S ? load16(a.S + (size_t)t * a.D + at[v]) : u32x4{0, 0, 0, 0};
+  };
+  auto load_post = [&](int v) __attribute__((always_inline)) {
+    vpost[v] = load16((a.post ? a.post : none) + at[v]);
+  };
+  auto load_gate = [&](int v) __attribute__((always_inline)) {
+    vgate[v] = load16(a.gate ? a.gate + (size_t)t * a.gate_ld + at[v] : none + at[v]);
+  };
+  auto load_pre = [&](int v) __attribute__((always_inline)) { vpre[v] = load16(a.pre + at[v]); };
+  auto load_x = [&](int v) __attribute__((always_inline)) {
+    const size_t p = (size_t)t * a.D + at[v];
+    if constexpr (XF32) {
+      vx[v] = load16((const float*)a.X + p);
+      vx2[v] = load16((const float*)a.X + p + 4);
+    } else {
+      vx[v] = load16((const uint16_t*)a.X + p);
+    }
+  };
+  if constexpr (kEarly) load_s(0), load_post(0), load_gate(0), load_pre(0), load_x(0);
   const uint16_t* B = a.B + (size_t)t * a.k * a.D;
   auto add = [&](const u32x4 (&b)[VPL], int j) __attribute__((always_inline)) {
     const bool there = a.experts[(size_t)t * a.k + j] >= 0;
@@ -118,7 +143,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void combine_norm_kernel(N
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       float f[8];
-      unpack8(load16(a.S + (size_t)t * a.D + at[v]), f);
+      if constexpr (!kEarly) load_s(v);
+      unpack8(vs[v], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[v][i] += f[i];
     }
@@ -133,7 +159,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void combine_norm_kernel(N
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       float f[8];
-      unpack8(load16(a.post + at[v]), f);
+      if constexpr (!kEarly) load_post(v);
+      unpack8(vpost[v], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[v][i] *= r * f[i];
     }
@@ -142,7 +169,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void combine_norm_kernel(N
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       float f[8];
-      unpack8(load16(a.gate + (size_t)t * a.gate_ld + at[v]), f);
+      if constexpr (!kEarly) load_gate(v);
+      unpack8(vgate[v], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[v][i] *= f[i];
     }
@@ -152,13 +180,13 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void combine_norm_kernel(N
   for (int v = 0; v < VPL; ++v) {
     const size_t p = (size_t)t * a.D + at[v];
     float x[8];
+    if constexpr (!kEarly) load_x(v);
     if constexpr (XF32) {
-      const f32x4 lo = __builtin_bit_cast(f32x4, load16((const float*)a.X + p));
-      const f32x4 hi = __builtin_bit_cast(f32x4, load16((const float*)a.X + p + 4));
+      const f32x4 lo = __builtin_bit_cast(f32x4, vx[v]), hi = __builtin_bit_cast(f32x4, vx2[v]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
     } else {
-      unpack8(load16((const uint16_t*)a.X + p), x);
+      unpack8(vx[v], x);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -179,7 +207,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void combine_norm_kernel(N
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     float f[8];
-    unpack8(load16(a.pre + at[v]), f);
+    if constexpr (!kEarly) load_pre(v);
+    unpack8(vpre[v], f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] *= r * o[v][i];
     if (in[v]) *reinterpret_cast<u32x4*>(a.H + (size_t)t * a.D + at[v]) = pack8(f);

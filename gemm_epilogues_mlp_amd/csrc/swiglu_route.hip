@@ -67,7 +67,7 @@ struct RouteArgs {
   int32_t* experts;
   int32_t* offsets;
   int32_t* rows;
-  int32_t* counts;  // workspace: [blocks, E]
+  int32_t* counts;  // workspace: [E, workgroups]
   int T, E, k, renorm;
   int vec;          // rows are 16-byte aligned and a multiple of 16 bytes
   int tokens;       // tokens of a workgroup
@@ -76,16 +76,17 @@ struct RouteArgs {
 // The experts of one token on G lanes (C logits each; lane order is index
 // order, so the lowest of several equal maxima is in the lowest lane that has
 // one).  Every lane takes part in the cross-lane steps; `in` says whether the
-// token exists.  Lane gl < k keeps choice gl, for k <= G.
+// token exists.  Lane gl < k ends up with choice gl, for k <= G.  The chain
+// from one choice to the next is the bound of a call, so it holds only what it
+// has to: the winner notes its index in `picked` (LDS, G places of this
+// token), the exponentials wait until all choices are known.
 template <typename In, int G, int C>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int t, bool in, int32_t& expert,
-                                            float& weight) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, bool in, int* picked,
+                                            int32_t& expert, float& weight) {
   const int lane = threadIdx.x & 63, gl = lane & (G - 1);
   float x[C];
   load_logits<C>((const In*)a.logits + (size_t)(in ? t : 0) * a.E, in ? a.E : 0, gl * C, a.vec, x);
-  float top = 0.0f, total = 0.0f;
-  expert = -1;
-  weight = 0.0f;
+  float top = 0.0f, total = 0.0f, mine = kNegInf;
   for (int i = 0; i < a.k; ++i) {
     float v = x[0];
     int bj = 0;
@@ -93,43 +94,49 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, bool in, 
     for (int j = 1; j < C; ++j)
       if (x[j] > v) v = x[j], bj = j;
     const float best = group_max<G>(v);
-    const bool open = best > kNegInf;
     if (i == 0) {
       // all E terms, before any is taken out; an infinite maximum (equal
       // shares of what is infinite) has no finite difference to itself
-      top = open ? best : 0.0f;
-      float s = 0.0f;
+      top = best > kNegInf ? best : 0.0f;
+      if (!a.renorm) {
+        float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < C; ++j) s += x[j] == top ? 1.0f : expf(x[j] - top);
-      total = a.renorm ? 0.0f : group_sum<G>(open ? s : 0.0f);
+        for (int j = 0; j < C; ++j) s += x[j] == top ? 1.0f : expf(x[j] - top);
+        total = group_sum<G>(s);
+      }
     }
+    if (gl == i) mine = best;
     const unsigned long long group = (G == 64 ? ~0ull : ((1ull << (G & 63)) - 1)) << (lane & ~(G - 1));
-    const int src = __ffsll(__ballot(v == best) & group) - 1;
-    const int idx = __shfl(gl * C + bj, src);
-    const float p = !open ? 0.0f : (best == top ? 1.0f : expf(best - top));
-    if (a.renorm) total += p;
-    if (gl == i) expert = open ? idx : -1, weight = p;
-    if (lane == src) {
+    if (lane == __ffsll(__ballot(v == best) & group) - 1) {
+      picked[i] = gl * C + bj;
 #pragma unroll
       for (int j = 0; j < C; ++j)
         if (j == bj) x[j] = kNegInf;
     }
   }
-  weight = total > 0.0f ? weight / total : 0.0f;
+  const bool open = mine > kNegInf;
+  const float p = !open ? 0.0f : (mine == top ? 1.0f : expf(mine - top));
+  if (a.renorm) total = group_sum<G>(p);
+  expert = open && gl < a.k ? picked[gl] : -1;  // written by this wave: in order
+  weight = open ? p / total : 0.0f;
 }
 
-// Tokens [t0, t1) by the workgroup: results to memory, slots counted in hist.
+// Tokens [t0, t1) by the workgroup: results to memory, slots counted in hist,
+// and with `slots` the choices kept in LDS too.
 template <typename In, int G, int C>
-__device__ __forceinline__ void route_tokens(const RouteArgs& a, int t0, int t1, int* hist) {
-  const int per = blockDim.x / G, gl = threadIdx.x & (G - 1);
-  for (int t = t0 + (int)threadIdx.x / G; t - (int)threadIdx.x / G < t1; t += per) {
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, int t0, int t1, int* picked,
+                                             int* hist, int* slots) {
+  const int per = blockDim.x / G, gl = threadIdx.x & (G - 1), first = (int)threadIdx.x / G;
+  for (int t = t0 + first; t - first < t1; t += per) {
     const bool in = t < t1;
     int32_t e;
     float w;
-    route_token<In, G, C>(a, t, in, e, w);
+    route_token<In, G, C>(a, t, in, picked + (threadIdx.x & ~(G - 1)), e, w);
     if (in && gl < a.k) {
-      a.experts[(size_t)t * a.k + gl] = e;
-      a.weights[(size_t)t * a.k + gl] = w;
+      const size_t s = (size_t)t * a.k + gl;
+      a.experts[s] = e;
+      a.weights[s] = w;
+      if (slots) slots[s] = e;
       if (e >= 0) atomicAdd(hist + e, 1);
     }
   }
@@ -147,14 +154,15 @@ __device__ __forceinline__ unsigned long long same_expert(int e, int E) {
 
 // Slots [s0, s1) into their places: `next` holds, for every wave and expert,
 // the next free place (already advanced past the earlier slots).
-__device__ __forceinline__ void route_place(const RouteArgs& a, int s0, int s1, int total, int* next) {
+__device__ __forceinline__ void route_place(const RouteArgs& a, const int32_t* experts, int s0,
+                                            int s1, int total, int* next) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
   const int per = ((s1 - s0 + nw - 1) / nw + 63) / 64 * 64;
   const int b = s0 + wave * per, e = min(b + per, s1);
   const int n = a.T * a.k;
   int* mine = next + wave * a.E;
   for (int s = b + lane; s - lane < e; s += 64) {
-    const int x = s < e ? a.experts[s] : -1;
+    const int x = s < e ? experts[s] : -1;
     const unsigned long long same = same_expert(x, a.E);
     if (x >= 0 && x < a.E) {
       const int rank = __popcll(same & ((1ull << lane) - 1));
@@ -168,12 +176,13 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, int s0, int s1, 
 }
 
 // Counts of each wave's share of [s0, s1) into next[wave][expert].
-__device__ __forceinline__ void route_count(const RouteArgs& a, int s0, int s1, int* next) {
+__device__ __forceinline__ void route_count(const RouteArgs& a, const int32_t* experts, int s0,
+                                            int s1, int* next) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
   const int per = ((s1 - s0 + nw - 1) / nw + 63) / 64 * 64;
   const int b = s0 + wave * per, e = min(b + per, s1);
   for (int s = b + lane; s < e; s += 64) {
-    const int x = a.experts[s];
+    const int x = experts[s];
     if (x >= 0 && x < a.E) atomicAdd(next + wave * a.E + x, 1);
   }
 }
@@ -206,71 +215,90 @@ __device__ __forceinline__ void route_bases(int* next, const int* base, int E) {
   }
 }
 
+// Slots that one workgroup still takes by itself: below this a second launch
+// costs more than the other workgroups' help gives.
+constexpr long long kRouteSmall = 512;
+
 // ---- one workgroup does everything -------------------------------------------------
-// Slots it wrote itself are read back behind a barrier of the workgroup, which
-// orders them.
 constexpr int kSmallThreads = 512;
 template <typename In, int G, int C>
 __global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a) {
   __shared__ __attribute__((aligned(16))) int next[kSmallThreads / 64 * G * C];
   __shared__ __attribute__((aligned(16))) int hist[G * C];
   __shared__ __attribute__((aligned(16))) int offset[G * C + 1];
+  __shared__ __attribute__((aligned(16))) int picked[kSmallThreads];
+  __shared__ __attribute__((aligned(16))) int slots[kRouteSmall];
   const int nw = kSmallThreads / 64, n = a.T * a.k;
   for (int i = threadIdx.x; i < nw * a.E; i += blockDim.x) next[i] = 0;
   for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
-  route_tokens<In, G, C>(a, 0, a.T, hist);
+  route_tokens<In, G, C>(a, 0, a.T, picked, hist, slots);
   __syncthreads();
-  route_count(a, 0, n, next);
+  route_count(a, slots, 0, n, next);
   route_scan(hist, offset, a.E);
   __syncthreads();
   route_bases(next, offset, a.E);
   for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = offset[i];
   __syncthreads();
-  route_place(a, 0, n, offset[a.E], next);
+  route_place(a, slots, 0, n, offset[a.E], next);
 }
 
 // ---- many tokens: choose and count, then place ---------------------------------------
-constexpr int kRouteThreads = 256;
+// The counts are [E, blocks] (rows of `stride` integers, a multiple of 4), so
+// that in the second launch one wave reads an expert's counts of all
+// workgroups with one 16-byte load a lane, all its experts' loads in flight
+// together (a loop over workgroups, a load each, took 34 us at 256 of them).
+constexpr int kSelectThreads = 512, kPlaceThreads = 1024;
+constexpr int kMaxRouteBlocks = 256;  // one 16-byte load of a wave
 template <typename In, int G, int C>
-__global__ __launch_bounds__(kRouteThreads) void route_select_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kSelectThreads) void route_select_kernel(RouteArgs a, int stride) {
   __shared__ __attribute__((aligned(16))) int hist[G * C];
+  __shared__ __attribute__((aligned(16))) int picked[kSelectThreads];
   for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
   const int t0 = blockIdx.x * a.tokens;
-  route_tokens<In, G, C>(a, t0, min(t0 + a.tokens, a.T), hist);
+  route_tokens<In, G, C>(a, t0, min(t0 + a.tokens, a.T), picked, hist, nullptr);
   __syncthreads();
-  for (int i = threadIdx.x; i < a.E; i += blockDim.x) a.counts[(size_t)blockIdx.x * a.E + i] = hist[i];
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x)
+    a.counts[(size_t)i * stride + blockIdx.x] = hist[i];
 }
 
 template <int EMAX>
-__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a) {
-  constexpr int NW = kRouteThreads / 64;
+__global__ __launch_bounds__(kPlaceThreads) void route_place_kernel(RouteArgs a, int stride) {
+  constexpr int NW = kPlaceThreads / 64, PER = EMAX / NW;  // experts a wave
   __shared__ __attribute__((aligned(16))) int next[NW * EMAX];
   __shared__ __attribute__((aligned(16))) int count[EMAX];
   __shared__ __attribute__((aligned(16))) int base[EMAX];
   __shared__ __attribute__((aligned(16))) int offset[EMAX + 1];
-  const int nb = gridDim.x, me = blockIdx.x;
+  const int nb = gridDim.x, me = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int i = threadIdx.x; i < NW * a.E; i += blockDim.x) next[i] = 0;
-  for (int i = threadIdx.x; i < a.E; i += blockDim.x) count[i] = base[i] = 0;
-  __syncthreads();
-  // every workgroup adds up the counts of all, and of those before it; the
-  // threads share the workgroups' rows, integer sums in any order
-  const int parts = a.E < kRouteThreads ? kRouteThreads / a.E : 1;
-  for (int i = threadIdx.x; i < parts * a.E; i += blockDim.x) {
-    const int x = i % a.E;
-    int all = 0, mine = 0;
-    for (int b = i / a.E; b < nb; b += parts) {
-      const int n = a.counts[(size_t)b * a.E + x];
-      all += n;
-      if (b < me) mine += n;
+  constexpr int STEP = PER < 8 ? PER : 8;  // loads in flight a lane
+  for (int j0 = 0; j0 < PER; j0 += STEP) {
+    u32x4 n[STEP];
+#pragma unroll
+    for (int j = 0; j < STEP; ++j) {
+      const int x = wave + NW * (j0 + j);
+      n[j] = x < a.E && 4 * lane < nb ? load16(a.counts + (size_t)x * stride + 4 * lane)
+                                      : u32x4{0, 0, 0, 0};
     }
-    atomicAdd(count + x, all);
-    atomicAdd(base + x, mine);
+#pragma unroll
+    for (int j = 0; j < STEP; ++j) {
+      int all = 0, mine = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int b = 4 * lane + q, v = b < nb ? (int)n[j][q] : 0;  // the last group's padding
+        all += v;
+        mine += b < me ? v : 0;
+      }
+      all = wave_scan(all);
+      mine = wave_scan(mine);
+      const int x = wave + NW * (j0 + j);
+      if (lane == 63 && x < a.E) count[x] = all, base[x] = mine;
+    }
   }
-  const int s0 = me * a.tokens * a.k, s1 = min(s0 + a.tokens * a.k, a.T * a.k);
-  route_count(a, s0, s1, next);
   __syncthreads();
+  const int s0 = me * a.tokens * a.k, s1 = min(s0 + a.tokens * a.k, a.T * a.k);
+  route_count(a, a.experts, s0, s1, next);
   route_scan(count, offset, a.E);
   __syncthreads();
   for (int x = threadIdx.x; x < a.E; x += blockDim.x) base[x] += offset[x];
@@ -279,25 +307,27 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
   if (me == 0)
     for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = offset[i];
   __syncthreads();
-  route_place(a, s0, s1, offset[a.E], next);
+  route_place(a, a.experts, s0, s1, offset[a.E], next);
 }
 
 // ---- launches ---------------------------------------------------------------------------
-// Slots that one workgroup still takes by itself: below this a second launch
-// costs more than the others' help gives.
-constexpr long long kRouteSmall = 512;
-
-static int route_blocks(long long T, long long* tokens) {
-  // about one workgroup a CU, at least 16 tokens each (one pass of its lanes)
-  long long per = (T + 255) / 256;
-  per = (per + 15) / 16 * 16;
+// Lanes a token: the fewest that hold E logits at 8 a lane, and k choices.
+static int route_lanes(long long E, long long k) {
+  return E <= 128 && k <= 16 ? 16 : (E <= 256 && k <= 32 ? 32 : 64);
+}
+// At most kMaxRouteBlocks workgroups, of at least the tokens that one pass of
+// their lanes takes.
+static int route_blocks(long long T, long long E, long long k, long long* tokens) {
+  const long long pass = kSelectThreads / route_lanes(E, k);
+  long long per = (T + kMaxRouteBlocks - 1) / kMaxRouteBlocks;
+  per = (per + pass - 1) / pass * pass;
   *tokens = per;
   return (int)((T + per - 1) / per);
 }
 long long route_workspace_bytes(long long T, long long E, long long k) {
   if (T * k <= kRouteSmall) return 0;
   long long tokens;
-  return (long long)route_blocks(T, &tokens) * E * 4;
+  return (route_blocks(T, E, k, &tokens) + 3LL) / 4 * 4 * E * 4;
 }
 
 template <typename In, int G, int C>
@@ -305,18 +335,18 @@ static hipError_t launch_route_as(RouteArgs a, hipStream_t stream) {
   if ((long long)a.T * a.k <= kRouteSmall)
     return launch_op(route_small_kernel<In, G, C>, dim3(1), dim3(kSmallThreads), stream, a);
   long long tokens;
-  const int blocks = route_blocks(a.T, &tokens);
+  const int blocks = route_blocks(a.T, a.E, a.k, &tokens), stride = (blocks + 3) / 4 * 4;
   a.tokens = (int)tokens;
-  const hipError_t e =
-      launch_op(route_select_kernel<In, G, C>, dim3(blocks), dim3(kRouteThreads), stream, a);
+  const hipError_t e = launch_op(route_select_kernel<In, G, C>, dim3(blocks), dim3(kSelectThreads),
+                                 stream, a, stride);
   if (e != hipSuccess) return e;
-  return launch_op(route_place_kernel<G * C>, dim3(blocks), dim3(kRouteThreads), stream, a);
+  return launch_op(route_place_kernel<G * C>, dim3(blocks), dim3(kPlaceThreads), stream, a, stride);
 }
 template <typename In>
 static hipError_t launch_route_in(const RouteArgs& a, hipStream_t stream) {
-  // lanes a token: the fewest that hold E logits at 8 a lane, and k choices
-  if (a.E <= 128 && a.k <= 16) return launch_route_as<In, 16, 8>(a, stream);
-  if (a.E <= 256 && a.k <= 32) return launch_route_as<In, 32, 8>(a, stream);
+  const int lanes = route_lanes(a.E, a.k);
+  if (lanes == 16) return launch_route_as<In, 16, 8>(a, stream);
+  if (lanes == 32) return launch_route_as<In, 32, 8>(a, stream);
   if (a.E <= 512) return launch_route_as<In, 64, 8>(a, stream);
   return launch_route_as<In, 64, 16>(a, stream);
 }

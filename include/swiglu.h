@@ -498,7 +498,7 @@ int64_t swiglu_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
  * The result does not depend on timing.  Limits: E <= 1024, k <= min(E, 64),
  * T k < 2^31 (else UNSUPPORTED; k > E: INVALID_ARG).  INVALID_ARG also for a
  * workspace too small and for overlapping tensors; pointers must be aligned to
- * their elements (else UNSUPPORTED). */
+ * their elements, the workspace to 16 bytes (else UNSUPPORTED). */
 swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weights,
                              int32_t* experts, int32_t* offsets, int32_t* rows, void* workspace,
                              int64_t workspace_bytes, int64_t T, int64_t E, int64_t k,
@@ -512,8 +512,8 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
  * [0, R] whatever offsets holds.  bf16 tensors, fp32 sums, one rounding.
  * N % 8 == 0, K % 8 == 0, 16-byte aligned tensors, A and one expert's weights
  * under 2 GiB, E <= 1024 (else UNSUPPORTED); all of W and Y may be larger.
- * variant < 0: the kernel is chosen from R / E; 0 ... 4 force one (tests and
- * tuning), another is INVALID_ARG. */
+ * variant < 0: the kernel is chosen from R, E and N; 0 ... 3 force one (tests
+ * and tuning), a larger one is INVALID_ARG. */
 swiglu_status_t swiglu_grouped_forward(swiglu_handle_t h, const void* A, const int32_t* rows,
                                        const int32_t* offsets, const void* W, void* Y, int64_t T,
                                        int64_t R, int64_t N, int64_t K, int64_t E, int64_t k,
@@ -580,8 +580,8 @@ swiglu_status_t swiglu_dequantize_mxfp4(swiglu_handle_t h, const void* Q, const 
 
 /* Y = bf16(SiLU(g) * u), g and u the Gate and Up products of activations
  * (Q, SQ) [M, K] and weights (W, SW) [2N, K] in MXFP4; exact products, fp32
- * sums.  N % 8 == 0, K % 32 == 0, 16-byte aligned tensors, the codes of each
- * under 2 GiB (else UNSUPPORTED); Y [M, N] must not overlap an input.
+ * sums.  N % 8 == 0, K % 32 == 0, K <= 2^22, 16-byte aligned tensors, the codes
+ * of each under 2 GiB (else UNSUPPORTED); Y [M, N] must not overlap an input.
  * variant < 0: chosen from M and N; 0 ... 4 force one (tests and tuning). */
 swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const void* SQ,
                                      const void* W, const void* SW, void* Y, int64_t M, int64_t N,
