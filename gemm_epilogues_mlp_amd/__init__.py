@@ -162,6 +162,8 @@ def _stream(stream) -> int | None:
         # torch's current stream as a plain handle: torch.cuda.current_stream()
         # builds a Stream object first, 2.9 of a small call's 6.5 us
         import torch
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream

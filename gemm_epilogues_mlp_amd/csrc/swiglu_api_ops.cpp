@@ -41,7 +41,7 @@ extern "C" {
 
 int64_t swiglu_route_workspace_bytes(int64_t T, int64_t E, int64_t k) {
   if (T < 0 || E < 1 || k < 1 || k > E || E > kMaxExperts || k > kMaxChoices ||
-      T > 0x7fffffffLL || T * k > 0x7fffffffLL)
+      T > checks::kMaxSlots || T * k > checks::kMaxSlots)
     return 0;
   return route_workspace_bytes(T, E, k);
 }

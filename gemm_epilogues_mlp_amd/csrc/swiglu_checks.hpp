@@ -16,6 +16,7 @@ namespace checks {
 constexpr int kOk = 0, kInvalid = 1, kUnsupported = 2;
 constexpr long long kMaxInt = 0x7fffffffLL;
 constexpr long long kMax2G = 1LL << 31;
+constexpr long long kMaxSlots = 1LL << 30;
 constexpr long long kMaxTotal = 1LL << 46;  // bytes of a tensor addressed with 64 bits
 
 struct Span {
@@ -55,8 +56,8 @@ inline int route(const void* logits, const void* weights, const void* experts, c
   if (T < 0 || E < 1 || k < 1 || k > E || (dtype != 0 && dtype != 1)) return kInvalid;
   if (!offsets) return kInvalid;
   if (T > 0 && (!logits || !weights || !experts || !rows)) return kInvalid;
-  if (E > kMaxExperts || k > kMaxChoices || T > kMaxInt || mul(T, k) > kMaxInt ||
-      mul(T, E) > kMaxTotal)
+  // 2^30 slots: the last workgroup's tokens are counted from past the last one
+  if (E > kMaxExperts || k > kMaxChoices || mul(T, k) > kMaxSlots || mul(T, E) > kMaxTotal)
     return kUnsupported;
   const unsigned size = dtype ? 4 : 2;
   for (const void* p : {weights, experts, offsets, rows})
@@ -82,7 +83,8 @@ inline int grouped(bool up, const void* A, const void* rows, const void* offsets
     return kOk;
   }
   if (!rows || !offsets || !Y || (K > 0 && (!W || (TA > 0 && !A)))) return kInvalid;
-  if (E > kMaxExperts || TA > kMaxInt || R > kMaxInt || K > kMaxInt || N > (kMaxInt >> 1) ||
+  // N: a K step's 32 rows past a matrix of under 2 GiB end within 32-bit offsets
+  if (E > kMaxExperts || TA > kMaxInt || R > kMaxInt || K > kMaxInt || N > (1LL << 23) ||
       k > kMaxInt || N % 8 != 0 || K % 8 != 0)
     return kUnsupported;
   if (!aligned16({A, W, Y}) || !aligned(rows, 4) || !aligned(offsets, 4)) return kUnsupported;

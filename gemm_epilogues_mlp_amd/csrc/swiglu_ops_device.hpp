@@ -63,6 +63,17 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
+// Inclusive maximum of the lanes up to and with this one, of v >= 0.
+__device__ __forceinline__ int wave_scan_max(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+  return v;
+}
+
 // ---- which expert a workgroup works on -----------------------------------------
 // Sorted rows [offsets[e], offsets[e + 1]) belong to expert e.  Each expert's
 // rows are cut into tiles of BM, the last one of as many parts (BM / PARTS
@@ -75,8 +86,9 @@ __device__ __forceinline__ int wave_scan(int v) {
 // tiles out behind all whole ones balances as well, but they then read every
 // expert's weights a second time: 1053 against 960 us for 32760 rows, 32
 // experts, 3584 x 4736 weights each.)
-// Offsets are held to [0, R] whatever the tensor says, so no row index leaves
-// the sorted range.
+// Whatever the tensor says, an offset is held to [0, R] and counts as the largest
+// one before it where it is below that: no row index leaves the sorted range, and
+// the spans never overlap, so there are never more than R rows in all.
 struct GroupUnit {
   int expert, first, rows;  // the expert, its first sorted row, its rows
   int local;                // unit number within the expert
@@ -84,13 +96,19 @@ struct GroupUnit {
 struct GroupRange {
   int begin, end;  // units of this XCD
 };
-__device__ __forceinline__ void group_span(const int32_t* offsets, int e, int E, int R, int& lo,
-                                           int& n) {
-  lo = n = 0;
+// this lane's span, of expert c + lane; `reach` is where the spans before c end
+// and becomes where those of this wave do
+__device__ __forceinline__ void group_span(const int32_t* offsets, int c, int E, int R, int& reach,
+                                           int& lo, int& n) {
+  const int e = c + (int)(threadIdx.x & 63);
+  int from = 0, to = 0;
   if (e < E) {
-    lo = min(max(offsets[e], 0), R);
-    n = max(min(offsets[e + 1], R) - lo, 0);
+    from = min(max(offsets[e], 0), R);
+    to = min(max(offsets[e + 1], 0), R);
   }
+  lo = max(wave_scan_max(from), reach);
+  n = max(to - lo, 0);
+  reach = __builtin_amdgcn_readlane(lo + n, 63);
 }
 template <int BM, int PARTS>
 __device__ __forceinline__ int group_work(int n) {
@@ -100,10 +118,9 @@ __device__ __forceinline__ int group_work(int n) {
 template <int BM, int PARTS>
 __device__ __forceinline__ GroupRange group_range(const int32_t* __restrict__ offsets, int E,
                                                   int R, int ntn, int x) {
-  const int lane = threadIdx.x & 63;
-  int lo, n, sum = 0;
+  int lo, n, sum = 0, reach = 0;
   for (int c = 0; c < E; c += 64) {
-    group_span(offsets, c + lane, E, R, lo, n);
+    group_span(offsets, c, E, R, reach, lo, n);
     sum += __builtin_amdgcn_readlane(wave_scan(group_work<BM, PARTS>(n)), 63);
   }
   // where an eighth of the work ends: the expert it falls into, and of its
@@ -111,8 +128,9 @@ __device__ __forceinline__ GroupRange group_range(const int32_t* __restrict__ of
   const long long work = (long long)sum * ntn;
   const long long at[2] = {work * x / 8, work * (x + 1) / 8};
   int cut[2] = {-1, -1}, before_p = 0, before_t = 0;
+  reach = 0;
   for (int c = 0; c < E; c += 64) {
-    if (E > 64) group_span(offsets, c + lane, E, R, lo, n);
+    if (E > 64) group_span(offsets, c, E, R, reach, lo, n);
     const int p = group_work<BM, PARTS>(n), t = (n + BM - 1) / BM;
     const int ip = wave_scan(p), it = wave_scan(t);
 #pragma unroll
@@ -135,12 +153,11 @@ __device__ __forceinline__ GroupRange group_range(const int32_t* __restrict__ of
 template <int BM>
 __device__ __forceinline__ GroupUnit group_unit(const int32_t* __restrict__ offsets, int E, int R,
                                                 int ntn, int t) {
-  const int lane = threadIdx.x & 63;
   GroupUnit u{0, 0, 0, 0};
-  int before = 0;
+  int before = 0, reach = 0;
   for (int c = 0; c < E; c += 64) {
     int lo, n;
-    group_span(offsets, c + lane, E, R, lo, n);
+    group_span(offsets, c, E, R, reach, lo, n);
     const int tiles = (n + BM - 1) / BM, incl = wave_scan(tiles);
     const unsigned long long past = __ballot((before + incl) * ntn > t);
     if (past) {

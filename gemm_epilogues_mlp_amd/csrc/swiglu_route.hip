@@ -114,6 +114,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, bool in, 
         if (j == bj) x[j] = kNegInf;
     }
   }
+  __builtin_amdgcn_wave_barrier();  // other lanes' notes: no read moves above this
   const bool open = mine > kNegInf;
   const float p = !open ? 0.0f : (mine == top ? 1.0f : expf(mine - top));
   if (a.renorm) total = group_sum<G>(p);
@@ -168,6 +169,7 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, const int32_t* e
       const int rank = __popcll(same & ((1ull << lane) - 1));
       const int at = mine[x] + rank;
       if (at >= 0 && at < n) a.rows[at] = s;
+      __builtin_amdgcn_wave_barrier();  // every lane has read its place
       if (rank == 0) mine[x] += __popcll(same);
     }
   }

@@ -496,7 +496,7 @@ int64_t swiglu_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
  * appear in no span; rows past offsets[E] are -1.  Where the largest logit is
  * +inf the infinite ones share the weight.  T = 0 writes the offsets.
  * The result does not depend on timing.  Limits: E <= 1024, k <= min(E, 64),
- * T k < 2^31 (else UNSUPPORTED; k > E: INVALID_ARG).  INVALID_ARG also for a
+ * T k <= 2^30 (else UNSUPPORTED; k > E: INVALID_ARG).  INVALID_ARG also for a
  * workspace too small and for overlapping tensors; pointers must be aligned to
  * their elements, the workspace to 16 bytes (else UNSUPPORTED). */
 swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weights,
@@ -508,10 +508,12 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
  * offsets[e + 1]), with a = A[rows[i] / k], A [T, K], W [E, K, 2N] holding G_e
  * in the even and U_e in the odd columns of expert e (the W_fused order), Y
  * [R, N] in sorted order.  Rows of Y in no span are not written; a slot that
- * names no row of A gives the products of a row of zeros.  Spans are held to
- * [0, R] whatever offsets holds.  bf16 tensors, fp32 sums, one rounding.
- * N % 8 == 0, K % 8 == 0, 16-byte aligned tensors, A and one expert's weights
- * under 2 GiB, E <= 1024 (else UNSUPPORTED); all of W and Y may be larger.
+ * names no row of A gives the products of a row of zeros.  Whatever offsets
+ * holds, each is held to [0, R] and counts as the largest before it where it is
+ * below that.  bf16 tensors, fp32 sums, one rounding.
+ * N % 8 == 0, K % 8 == 0, N <= 2^23, 16-byte aligned tensors, A and one
+ * expert's weights under 2 GiB, E <= 1024 (else UNSUPPORTED); all of W and Y may
+ * be larger.
  * variant < 0: the kernel is chosen from R, E and N; 0 ... 3 force one (tests
  * and tuning), a larger one is INVALID_ARG. */
 swiglu_status_t swiglu_grouped_forward(swiglu_handle_t h, const void* A, const int32_t* rows,

@@ -204,6 +204,29 @@ def test_bad_offsets_and_slots_stay_inside(handle, variant):
     O.assert_close(Y[33:R], want, slack, "down")
 
 
+@pytest.mark.parametrize("variant", range(4))
+def test_overlapping_offsets_count_once(handle, variant):
+    """An offset below an earlier one counts as that one: every row has one expert, and the
+    units never exceed those of R rows."""
+    R, N, K, E = 300, 72, 40, 100
+    off = torch.full((E + 1,), R, dtype=torch.int32)
+    off[0::2] = 0                              # taken as they are: 50 spans of all rows
+    off[:4] = torch.tensor([0, 40, 10, 30])
+    off[4] = 170
+    ends = np.maximum.accumulate(np.clip(off.numpy(), 0, R))
+    rows = torch.arange(R, dtype=torch.int32)
+    A, W = randn(1, R, K), randn(2, E, K, 2 * N, std=K ** -0.5)
+    Y = torch.full((R, N), -7.0, dtype=BF, device="cuda")
+    sw.swiglu_grouped_forward(handle, A.cuda(), rows.cuda(), off.cuda(), W.cuda(), Y, R, R, N, K, E,
+                              variant=variant)
+    torch.cuda.synchronize()
+    for e in range(E):
+        a, b = int(ends[e]), int(ends[e + 1])
+        if b > a:
+            want, slack = O.gated(A[a:b], W[e])
+            O.assert_close(Y[a:b], want, slack, f"expert {e}")
+
+
 def test_weights_past_4_gib(handle):
     """The last expert of a stack whose byte offsets pass 32 bits."""
     E, N, K = 40, 4096, 8192
