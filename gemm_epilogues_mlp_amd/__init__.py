@@ -152,19 +152,28 @@ def _ptr(x) -> int | None:
     """Device pointer of a tensor (data_ptr), an int address, or None."""
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+        raise
+
+
+_torch_c = None  # torch._C, once torch has set the device up
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         # torch's current stream as a plain handle: torch.cuda.current_stream()
         # builds a Stream object first, 2.9 of a small call's 6.5 us
-        import torch
-        if not torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        global _torch_c
+        if _torch_c is None:
+            import torch
+            if not torch.cuda.is_initialized():
+                return torch.cuda.current_stream().cuda_stream
+            _torch_c = torch._C
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

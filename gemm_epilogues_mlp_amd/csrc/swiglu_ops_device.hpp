@@ -4,6 +4,7 @@
 #pragma once
 
 #include <tuple>
+#include <type_traits>
 
 #include "swiglu_device.hpp"
 
@@ -32,6 +33,19 @@ __device__ __forceinline__ float group_max(float v) {
   if (G >= 16) v = fmaxf(v, dpp_f<kDppMirror>(v));
   if (G >= 32) v = fmaxf(v, __shfl_xor(v, 16));
   if (G >= 64) v = fmaxf(v, __shfl_xor(v, 32));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  auto dpp = [](auto ctrl, uint32_t x) __attribute__((always_inline)) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, decltype(ctrl)::value, 0xf, 0xf, false);
+  };
+  v = max(v, dpp(std::integral_constant<int, kDppXor1>{}, v));
+  v = max(v, dpp(std::integral_constant<int, kDppXor2>{}, v));
+  if (G >= 8) v = max(v, dpp(std::integral_constant<int, kDppHalfMirror>{}, v));
+  if (G >= 16) v = max(v, dpp(std::integral_constant<int, kDppMirror>{}, v));
+  if (G >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+  if (G >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
   return v;
 }
 template <int G>
