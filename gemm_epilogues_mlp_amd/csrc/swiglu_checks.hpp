@@ -83,7 +83,7 @@ inline int grouped(bool up, const void* A, const void* rows, const void* offsets
     return kOk;
   }
   if (!rows || !offsets || !Y || (K > 0 && (!W || (TA > 0 && !A)))) return kInvalid;
-  // N: a K step's 32 rows past a matrix of under 2 GiB end within 32-bit offsets
+  // N: a K step's 64 rows past a matrix of under 2 GiB end within 32-bit offsets
   if (E > kMaxExperts || TA > kMaxInt || R > kMaxInt || K > kMaxInt || N > (1LL << 23) ||
       k > kMaxInt || N % 8 != 0 || K % 8 != 0)
     return kUnsupported;

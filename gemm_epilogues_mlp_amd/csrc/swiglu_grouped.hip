@@ -55,12 +55,14 @@ __device__ __forceinline__ int group_a_row(const GroupArgs& g, int pos) {
 // matrix instructions, with one barrier a step; weight fragments are read with
 // the transposing LDS read, activation fragments with 16-byte reads, both from
 // XOR-swizzled chunks so that the lanes served together hit distinct banks.
+// With KG = 2 a step is 64 k, 32 of them for each of two groups of waves, whose
+// sums are added in LDS at the end: twice the waves for a small tile.
 // Rows past the span, columns past the matrix and k past K arrive as zeros (a
 // buffer load past the resource returns 0).
-template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN>
+template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int KG = 1>
 struct GroupTile {
-  static constexpr int BK = 32;
-  static constexpr int kThreads = 64 * WGM * WGN;
+  static constexpr int BK = 32 * KG;
+  static constexpr int kThreads = 64 * WGM * WGN * KG;
   static constexpr int BNY = OP == GROUP_UP ? BNW / 2 : BNW;
   static constexpr int WTM = BM / WGM, WTW = BNW / WGN;  // a wave's rows and columns
   static constexpr int FA = WTM / 32, FW = WTW / 32;
@@ -81,11 +83,15 @@ struct GroupTile {
   static constexpr int JUNK = STAGES * STAGE_BYTES;
   static constexpr int RING = JUNK + (NEED_JUNK ? 1024 : 0);
   static constexpr int Y_BYTES = BM * YLD * 2;
-  static constexpr int LDS_BYTES = RING > Y_BYTES ? RING : Y_BYTES;
+  // behind it, the sums of the wave groups on other k
+  static constexpr int RED_BYTES = (KG - 1) * BM * BNW * 4;
+  static constexpr int END = Y_BYTES + RED_BYTES;
+  static constexpr int LDS_BYTES = RING > END ? RING : END;
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
   // chunk c of row r is stored at c ^ swz(r): 64-byte rows of A; weight rows
   // that are an odd multiple of 128 bytes alternate halves of 256 by themselves
   __host__ __device__ static constexpr int a_swz(int row) {
+    if (ACH == 8) return (row >> 1) & 7;  // 128-byte rows: eight pairs of them
     return (((row >> 2) & 1) << 1) | (((row >> 1) ^ (row >> 3)) & 1);
   }
   __host__ __device__ static constexpr int w_swz(int row) {
@@ -97,10 +103,10 @@ struct GroupTile {
 
 // Rows [pos0, pos0 + nrows) (nrows <= BM) of expert `e` against weight columns
 // [tn BNW, (tn + 1) BNW).
-template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN>
+template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int KG = 1>
 __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0, int nrows,
                                              int tn, uint8_t* smem) {
-  using C = GroupTile<OP, BM, BNW, STAGES, WGM, WGN>;
+  using C = GroupTile<OP, BM, BNW, STAGES, WGM, WGN, KG>;
   constexpr int BK = C::BK;
   // a copy of the thread index that the compiler cannot see through: else it
   // keeps the offsets of every tile height in registers around the loop over
@@ -109,7 +115,8 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, wave = tid >> 6;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
-  const int wm = wave / WGN, wn = wave % WGN;
+  const int kg = wave / (WGM * WGN);  // which 32 k of a step
+  const int wm = wave / WGN % WGM, wn = wave % WGN;
   const int K = g.K, ldw = g.ldw;
   const int wc0 = tn * BNW;
   const int nk = (K + BK - 1) / BK;
@@ -155,10 +162,10 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
 
   // ---- fragments --------------------------------------------------------------------
   const int g16 = lane >> 4, s16 = lane & 15;
-  const int w_row = 8 * (g16 >> 1) + (s16 >> 2);
+  const int w_row = 32 * kg + 8 * (g16 >> 1) + (s16 >> 2);
   const int w_col = wn * C::WTW + 16 * (g16 & 1) + 4 * (s16 & 3);
   const int a_row = wm * C::WTM + (lane & 31);
-  const int a_chk = lane >> 5;
+  const int a_chk = 4 * kg + (lane >> 5);
   constexpr int NFRAG = 2 * C::FW + C::FA;
   u32x4 wf[2][C::FW], af[2][C::FA];
   auto frag = [&](auto st_c, int sub, int fb, int r) __attribute__((always_inline)) {
@@ -257,11 +264,40 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
   wait_vmcnt<0>();
   __syncthreads();
   uint16_t* ys = reinterpret_cast<uint16_t*>(smem);  // [BM][YLD]
+  if constexpr (KG > 1) {
+    // the groups' sums are added in their order
+    f32x4* red = reinterpret_cast<f32x4*>(smem + C::Y_BYTES);
+    constexpr int NQ = C::FW * C::FA * 4, WAVES = WGM * WGN;
+    const int w = wave % WAVES;
+    if (kg > 0) {
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+        const f32x16& d = acc[x / 4 / C::FA][x / 4 % C::FA];
+        const int r = x % 4 * 4;
+        red[(((kg - 1) * WAVES + w) * NQ + x) * 64 + lane] = f32x4{d[r], d[r + 1], d[r + 2], d[r + 3]};
+      }
+    }
+    __syncthreads();
+    if (kg == 0) {
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+        f32x16& d = acc[x / 4 / C::FA][x / 4 % C::FA];
+        const int r = x % 4 * 4;
+#pragma unroll
+        for (int o = 0; o < KG - 1; ++o) {
+          const f32x4 v = red[((o * WAVES + w) * NQ + x) * 64 + lane];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) d[r + q] += v[q];
+        }
+      }
+    }
+  }
   const int h32 = lane >> 5;
 #pragma unroll
   for (int i = 0; i < C::FW; ++i)
 #pragma unroll
     for (int j = 0; j < C::FA; ++j) {
+      if (KG > 1 && kg > 0) continue;
       const f32x16& d = acc[i][j];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -296,10 +332,11 @@ __device__ __forceinline__ void grouped_tile(const GroupArgs& g, int e, int pos0
 // tiles an eighth of the work may be more than an eighth of the units.  The
 // last tile of an expert runs at the height that its rows need (fewer matrix
 // instructions).
-template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN>
-__global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupArgs g, int ntn) {
+template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN,
+          int KG>
+__global__ __launch_bounds__(64 * WGM * WGN * KG) void grouped_tile_kernel(GroupArgs g, int ntn) {
   constexpr int P = BM / PARTS;  // rows of a part
-  constexpr int LDS = GroupTile<OP, BM, BNW, STAGES, WGM, WGN>::LDS_BYTES + (PARTS > 1 ? 1024 : 0);
+  constexpr int LDS = GroupTile<OP, BM, BNW, STAGES, WGM, WGN, KG>::LDS_BYTES + (PARTS > 1 ? 1024 : 0);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
   const GroupRange range = group_range<BM, PARTS>(g.offsets, g.E, g.R, ntn, blockIdx.x % 8);
   const int nwg = ((int)gridDim.x + 7 - (int)(blockIdx.x % 8)) / 8;  // of this XCD
@@ -310,18 +347,18 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupArgs 
     const int band = u.local / (kBand * ntn), in = u.local % (kBand * ntn);
     const int high = min(ntm - band * kBand, kBand);
     const int tm = band * kBand + in % high, tn = in / high;
-    const int pos0 = u.first + tm * BM, left = u.rows - tm * BM;
-    const int parts = (min(left, BM) + P - 1) / P;
+    const int pos0 = u.first + tm * BM, rows = min(u.rows - tm * BM, BM);
+    const int parts = (rows + P - 1) / P;
     auto part = [&](auto n_c) __attribute__((always_inline)) {
       constexpr int ROWS = decltype(n_c)::value * P;
       // short tiles: the waves side by side where two rows of them do not fit
       constexpr int WM = ROWS / 32 >= PWGM && ROWS % (32 * PWGM) == 0 ? PWGM : 1;
       constexpr int WN = PWGM * PWGN / WM;
-      static_assert(GroupTile<OP, ROWS, BNW, STAGES, WM, WN>::LDS_BYTES <= LDS, "LDS");
-      grouped_tile<OP, ROWS, BNW, STAGES, WM, WN>(g, u.expert, pos0, left, tn, smem);
+      static_assert(GroupTile<OP, ROWS, BNW, STAGES, WM, WN, KG>::LDS_BYTES <= LDS, "LDS");
+      grouped_tile<OP, ROWS, BNW, STAGES, WM, WN, KG>(g, u.expert, pos0, rows, tn, smem);
     };
     if (parts == PARTS) {
-      grouped_tile<OP, BM, BNW, STAGES, WGM, WGN>(g, u.expert, pos0, min(left, BM), tn, smem);
+      grouped_tile<OP, BM, BNW, STAGES, WGM, WGN, KG>(g, u.expert, pos0, rows, tn, smem);
     } else if (PARTS >= 4 && parts == 3) {
       if constexpr (PARTS >= 4) part(std::integral_constant<int, 3>{});
     } else if (PARTS >= 4 && parts == 2) {
@@ -441,7 +478,8 @@ static long long max_row_tiles(long long R, long long E, long long bm) {
   return std::min(R, (R + some * (bm - 1)) / bm);
 }
 
-template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN>
+template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN,
+          int KG = 1>
 static hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
   static_assert(WGM * WGN == PWGM * PWGN && (PARTS == 1 || PARTS == 2 || PARTS == 4), "one workgroup");
   const long long ntn = (g.ldw + BNW - 1) / BNW;
@@ -452,8 +490,8 @@ static hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
   const long long units = max_row_tiles(g.R, g.E, BM) * ntn;
   const long long grid = (units * (PARTS > 1 && units < 1024 ? 2 : 1) + 7) / 8 * 8;
   if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-  return launch_op(grouped_tile_kernel<OP, BM, BNW, STAGES, WGM, WGN, PARTS, PWGM, PWGN>,
-                   dim3((unsigned)grid), dim3(64 * WGM * WGN), stream, g, (int)ntn);
+  return launch_op(grouped_tile_kernel<OP, BM, BNW, STAGES, WGM, WGN, PARTS, PWGM, PWGN, KG>,
+                   dim3((unsigned)grid), dim3(64 * WGM * WGN * KG), stream, g, (int)ntn);
 }
 template <int OP, int MT, int NW>
 static hipError_t launch_stream(const GroupArgs& g, hipStream_t stream) {
@@ -472,6 +510,7 @@ static hipError_t launch_grouped_op(const GroupArgs& g, int variant, hipStream_t
     case 0: return launch_stream<OP, 1, 8>(g, stream);
     case 1: return launch_tile<OP, 64, 128, 4, 2, 2, 1, 2, 2>(g, stream);
     case 2: return launch_tile<OP, 128, 128, 4, 2, 2, 2, 2, 2>(g, stream);
+    case 4: return launch_tile<OP, 64, 64, 4, 2, 1, 1, 2, 1, 2>(g, stream);
     default: return launch_tile<OP, 256, 256, 4, 4, 2, 4, 2, 4>(g, stream);
   }
 }
@@ -480,12 +519,20 @@ static hipError_t launch_grouped_op(const GroupArgs& g, int variant, hipStream_t
 // there is a workgroup for every CU.  Measured (us, 2048 x 2816 weights, 32
 // experts, variants 0 / 1 / 3): mean 8: 61 / 70 / 75, 24: 114 / 72 / 78, 64: 244
 // / 93 / 80.  With few units the wide tiles stream better (8 experts, 3584 x
-// 4736, mean 8, 0 / 3: 57 / 52), and where even those leave CUs idle the
-// 128-row ones (8 experts, 2368 x 3584, mean 8, 0 / 2 / 3: 26.6 / 22.0 / 25.4).
+// 4736, mean 8, 0 / 3: 57 / 52).  Where even those leave CUs idle the bytes that
+// one CU can take in bound the call (about 50 a ns measured, however many loads
+// are in flight), so the tiles get smaller until there are about as many as CUs:
+// variants 1 / 2 / 4 take 44.9 / 35.8 / 43.4 us with 168 tiles of 128 x 128 (4
+// experts, 3416 x 816, mean 644), 24.9 / 31.7 / 27.9 with 112 of them (3584 x
+// 1792, mean 250), and 22.7 / 29.4 / 14.7 with 84 of 64 x 128 (3584 x 896, mean
+// 150).
 static int grouped_variant(long long R, long long E, long long ldw) {
   const long long some = std::min(R, E), mean = (R + E - 1) / E;
-  const long long wide = some * ((mean + 255) / 256) * ((ldw + 255) / 256);
-  if (wide < 128) return 2;
+  auto units = [&](long long bm, long long bnw) {
+    return some * ((mean + bm - 1) / bm) * ((ldw + bnw - 1) / bnw);
+  };
+  const long long wide = units(256, 256);
+  if (wide < 128) return units(64, 128) <= 128 ? 4 : (units(128, 128) <= 128 ? 1 : 2);
   if (wide >= 200 && mean <= 10) return 0;
   if (wide >= 200 && mean <= 28) return 1;
   return 3;

@@ -119,7 +119,7 @@ hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* e
                         int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
                         bool renorm, hipStream_t stream);
 // Grouped products; TA: rows of A, variant < 0: by rule
-constexpr int kGroupedVariants = 4;
+constexpr int kGroupedVariants = 5;
 hipError_t launch_grouped(bool up, const uint16_t* A, const int32_t* rows, const int32_t* offsets,
                           const uint16_t* W, uint16_t* Y, int TA, int R, int N, int K, int E,
                           int k, int variant, hipStream_t stream);

@@ -514,7 +514,7 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
  * N % 8 == 0, K % 8 == 0, N <= 2^23, 16-byte aligned tensors, A and one
  * expert's weights under 2 GiB, E <= 1024 (else UNSUPPORTED); all of W and Y may
  * be larger.
- * variant < 0: the kernel is chosen from R, E and N; 0 ... 3 force one (tests
+ * variant < 0: the kernel is chosen from R, E and N; 0 ... 4 force one (tests
  * and tuning), a larger one is INVALID_ARG. */
 swiglu_status_t swiglu_grouped_forward(swiglu_handle_t h, const void* A, const int32_t* rows,
                                        const int32_t* offsets, const void* W, void* Y, int64_t T,

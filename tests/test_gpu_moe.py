@@ -123,7 +123,7 @@ COUNTS = {"ones": [1, 1, 1], "empty": [0, 3, 0, 0, 17, 0], "tile": [16, 64, 0, 3
 UP_SHAPES = [(8, 8), (72, 40), (136, 200), (264, 520)]
 
 
-@pytest.mark.parametrize("variant", [-1, 0, 1, 2, 3])
+@pytest.mark.parametrize("variant", [-1, 0, 1, 2, 3, 4])
 @pytest.mark.parametrize("name", COUNTS)
 @pytest.mark.parametrize("N,K", UP_SHAPES)
 def test_grouped(handle, N, K, name, variant):
@@ -160,7 +160,7 @@ def test_grouped(handle, N, K, name, variant):
     assert bool((Y.cpu()[~seen] == -7.0).all()), "wrote a slot of no span"
 
 
-@pytest.mark.parametrize("variant", range(4))
+@pytest.mark.parametrize("variant", range(5))
 def test_rows_of_other_experts_do_not_leak(handle, variant):
     """NaN everywhere but in the rows and weights of one expert."""
     R, off, rows = spans([40, 70, 30], 3)
@@ -177,7 +177,7 @@ def test_rows_of_other_experts_do_not_leak(handle, variant):
     O.assert_close(Y[40:110], want, slack, "leak")
 
 
-@pytest.mark.parametrize("variant", range(4))
+@pytest.mark.parametrize("variant", range(5))
 def test_bad_offsets_and_slots_stay_inside(handle, variant):
     """Offsets past R are held to it, slots that name no row give zeros (up) or are not
     written (down)."""
@@ -204,7 +204,7 @@ def test_bad_offsets_and_slots_stay_inside(handle, variant):
     O.assert_close(Y[33:R], want, slack, "down")
 
 
-@pytest.mark.parametrize("variant", range(4))
+@pytest.mark.parametrize("variant", range(5))
 def test_overlapping_offsets_count_once(handle, variant):
     """An offset below an earlier one counts as that one: every row has one expert, and the
     units never exceed those of R rows."""
@@ -234,7 +234,7 @@ def test_weights_past_4_gib(handle):
     assert W.numel() * 2 > 2 ** 32
     w = randn(5, K, 2 * N, std=K ** -0.5)
     W[E - 1] = w.cuda()
-    for R, variant in ((3, 0), (3, 2), (3, 3)):
+    for R, variant in ((3, 0), (3, 2), (3, 3), (3, 4)):
         off = torch.zeros(E + 1, dtype=torch.int32)
         off[E] = R
         A = randn(6, R, K)
@@ -250,7 +250,7 @@ def test_grouped_empty_sizes(handle):
     sw.swiglu_grouped_forward(handle, None, None, None, None, None, 0, 0, 8, 8, 4)
     Y = torch.full((2, 8), 3.0, dtype=BF, device="cuda")
     off, rows = torch.tensor([0, 2], dtype=torch.int32).cuda(), torch.tensor([1, 0], dtype=torch.int32).cuda()
-    for variant in range(4):
+    for variant in range(5):
         Y.fill_(3.0)
         sw.swiglu_grouped_matmul(handle, None, rows, off, None, Y, 2, 8, 0, 1, variant=variant)
         torch.cuda.synchronize()
@@ -308,7 +308,7 @@ def test_refusals_write_nothing(handle):
         k=o.get("k", 1), variant=o.get("variant", -1))
     bad = [(dict(A=None), 1), (dict(rows=None), 1), (dict(off=None), 1), (dict(W=None), 1),
            (dict(Y=None), 1), (dict(Y=A), 1), (dict(k=0), 1), (dict(E=0), 1), (dict(R=-1), 1),
-           (dict(variant=4), 1), (dict(N=12), 2), (dict(K=12), 2), (dict(E=2000), 2),
+           (dict(variant=5), 1), (dict(N=12), 2), (dict(K=12), 2), (dict(E=2000), 2),
            (dict(A=A.view(-1)[4:]), 2), (dict(T=2 ** 27), 2)]
     for o, status in bad:
         with pytest.raises(sw.SwiGLUError) as err:

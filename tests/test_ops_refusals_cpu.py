@@ -67,7 +67,7 @@ def grouped_cases(up):
         (dict(h=None), INVALID), (dict(A=None), INVALID), (dict(rows=None), INVALID),
         (dict(off=None), INVALID), (dict(W=None), INVALID), (dict(Y=None), INVALID),
         (dict(R=-1), INVALID), (dict(N=-8), INVALID), (dict(K=-8), INVALID), (dict(E=0), INVALID),
-        (dict(variant=4), INVALID), (dict(N=60), UNSUPPORTED), (dict(K=36), UNSUPPORTED),
+        (dict(variant=5), INVALID), (dict(N=60), UNSUPPORTED), (dict(K=36), UNSUPPORTED),
         (dict(E=1025), UNSUPPORTED), (dict(A=P[0] + 8), UNSUPPORTED), (dict(W=P[3] + 8), UNSUPPORTED),
         (dict(Y=P[4] + 2), UNSUPPORTED), (dict(rows=P[1] + 2), UNSUPPORTED),
         (dict(off=P[2] + 1), UNSUPPORTED), (dict(N=(1 << 23) + 8, K=8), UNSUPPORTED),
@@ -75,7 +75,7 @@ def grouped_cases(up):
         (dict(R=1 << 40), UNSUPPORTED), (dict(N=1 << 62), UNSUPPORTED),
         (dict(Y=P[0]), INVALID), (dict(Y=P[3] + 64), INVALID), (dict(Y=P[1]), INVALID),
         (dict(R=0, A=None, rows=None, off=None, W=None, Y=None), OK), (dict(N=0, Y=None), OK),
-        (dict(K=0, A=None, W=None), DEVICE), (dict(variant=3), DEVICE),
+        (dict(K=0, A=None, W=None), DEVICE), (dict(variant=4), DEVICE),
         (dict(E=1000, K=4096, N=4096), DEVICE),          # 32 GiB and more of experts
     ]
 
