@@ -135,7 +135,7 @@ swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const voi
   bool noop;
   const int c = checks::forward_mxfp4(call, &noop);
   if (c != checks::kOk || noop) return (swiglu_status_t)c;
-  if ((variant >= 0 && variant <= 2) && (M + 31) / 32 > 65535) return SWIGLU_ERR_UNSUPPORTED;
+  if ((variant == 0 || variant == 1) && (M + 31) / 32 > 65535) return SWIGLU_ERR_UNSUPPORTED;
   const swiglu_status_t st = check_device(h);
   if (st != SWIGLU_OK) return st;
   return launched(launch_forward_mxfp4(call, variant, stream));

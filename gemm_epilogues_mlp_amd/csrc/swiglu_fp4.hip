@@ -364,7 +364,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void fp4_tile_kernel(
 // its NW waves take every NW-th group of 256 k, all of a group's loads (4 KB of
 // codes and 256 bytes of scales for each block) issued before its
 // first product.  The waves' fp32 sums are added in LDS in wave order, then
-// SiLU.  The weights are read once for every 32 MT rows.
+// SiLU.  The weights are read once for every 32 MT rows.  Eight waves: four gave
+// 16.0 instead of 15.2 us at 16 x 18944 x 3584, 7.3 instead of 5.9 at 50 x 4000 x
+// 3584.
 template <int MT, int NW>
 __global__ __launch_bounds__(64 * NW) void fp4_stream_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ W,
@@ -440,22 +442,33 @@ static hipError_t launch_f4_stream(const Fp4Call& c, hipStream_t stream) {
                    stream, c.A, c.SA, c.W, c.SW, c.Y, (int)c.M, (int)c.N, (int)c.K);
 }
 
-static int fp4_variant(long long M, long long N) {
+// Few rows stream the weights, and so do calls too small to give a quarter of
+// the CUs a small tile (us, variants 1 / 2: 50 x 4000 x 3584 5.9 / 9.8, 300 x 800 x
+// 3584 6.5 / 9.7, 100 x 2400 x 3584 9.1 / 9.7, 2000 x 200 x 2048 8.7 / 7.2, 64 x 18944 x
+// 3584 19.9 / 17.4).
+// Otherwise the large tiles (one workgroup a CU)
+// run 1.25 times as fast as the small ones (two a CU), but in whole rounds: of
+// the time of one large tile, they take ceil(tiles / CUs), the small ones about
+// 0.59 for every two a CU and half of that more for the end.  Measured (us,
+// large / small): 8192 x 18944 x 3584 542 / 659 (18.5 rounds), 4620 x 1528 x 1504
+// 18.7 / 22.3 (0.9), 1024 x 4864 x 896 11.9 / 10.3 (0.6), 2048 x 8960 x 1536 45.0 /
+// 39.6 (2.2), 512 x 18944 x 3584 53.1 / 43.4 (1.2).
+static int fp4_variant(long long M, long long N, int cu_count) {
   auto tiles = [&](long long bm, long long bny) { return (M + bm - 1) / bm * ((N + bny - 1) / bny); };
+  const long long small = tiles(128, 64), large = tiles(256, 128), cus = std::max(cu_count, 1);
   if (M <= 32) return 0;
-  if (M <= 64) return 1;
-  if (tiles(256, 128) >= 200) return 4;
-  if (tiles(128, 64) >= 200 || M > 512) return 3;
-  return 2;
+  if (small < (M <= 64 ? 200 : 64)) return 1;
+  const double t_large = (double)((large + cus - 1) / cus);
+  const double t_small = 0.59 * ((double)small / (2.0 * cus) + 0.5);
+  return t_large <= t_small ? 3 : 2;
 }
 
 hipError_t launch_forward_mxfp4(const Fp4Call& c, int variant, hipStream_t stream) {
-  if (variant < 0) variant = fp4_variant(c.M, c.N);
+  if (variant < 0) variant = fp4_variant(c.M, c.N, c.cu_count);
   switch (variant) {
-    case 0: return launch_f4_stream<1, 4>(c, stream);
-    case 1: return launch_f4_stream<2, 4>(c, stream);
-    case 2: return launch_f4_stream<4, 4>(c, stream);
-    case 3: return launch_f4_tile<128, 128, 2, 2>(c, stream);
+    case 0: return launch_f4_stream<1, 8>(c, stream);
+    case 1: return launch_f4_stream<2, 8>(c, stream);
+    case 2: return launch_f4_tile<128, 128, 2, 2>(c, stream);
     default: return launch_f4_tile<256, 256, 2, 4>(c, stream);
   }
 }

@@ -150,7 +150,7 @@ struct Fp4Call {
   long long M, N, K;
   int cu_count;
 };
-constexpr int kFp4Variants = 5;
+constexpr int kFp4Variants = 4;
 hipError_t launch_forward_mxfp4(const Fp4Call& c, int variant, hipStream_t stream);
 hipError_t launch_quantize_mxfp4(const uint16_t* X, uint8_t* Q, uint8_t* S, int rows, int K,
                                  hipStream_t stream);

@@ -584,7 +584,7 @@ swiglu_status_t swiglu_dequantize_mxfp4(swiglu_handle_t h, const void* Q, const 
  * (Q, SQ) [M, K] and weights (W, SW) [2N, K] in MXFP4; exact products, fp32
  * sums.  N % 8 == 0, K % 32 == 0, K <= 2^22, 16-byte aligned tensors, the codes
  * of each under 2 GiB (else UNSUPPORTED); Y [M, N] must not overlap an input.
- * variant < 0: chosen from M and N; 0 ... 4 force one (tests and tuning). */
+ * variant < 0: chosen from M and N; 0 ... 3 force one (tests and tuning). */
 swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const void* SQ,
                                      const void* W, const void* SW, void* Y, int64_t M, int64_t N,
                                      int64_t K, int32_t variant, hipStream_t stream);

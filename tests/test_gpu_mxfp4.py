@@ -119,7 +119,7 @@ SHAPES = [(1, 8, 32), (5, 24, 64), (33, 72, 96), (64, 136, 256), (130, 264, 288)
           (300, 128, 1056)]
 
 
-@pytest.mark.parametrize("variant", [-1, 0, 1, 2, 3, 4])
+@pytest.mark.parametrize("variant", [-1, 0, 1, 2, 3])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_product(handle, variant, shape):
     print(f"mxfp4 product {shape} variant {variant}", flush=True)
@@ -139,7 +139,7 @@ def test_product_scales_far_apart(handle):
     rng = np.random.default_rng(5)
     M, K = 96, 512
     x = rng.standard_normal((M, K // 32, 32)) * np.exp2(rng.integers(-20, 20, (M, K // 32, 1)))
-    for variant in range(5):
+    for variant in range(4):
         y, (want, slack) = product(handle, M, 64, K, variant, 6, bf16(x.reshape(M, K)))
         O.assert_close(y, want, slack, f"variant {variant}")
 
@@ -149,7 +149,7 @@ def test_nan_reaches_its_row_only(handle):
     M, N, K = 70, 40, 128
     x = bf16(rng.standard_normal((M, K)))
     x[37, 70] = float("nan")
-    for variant in range(5):
+    for variant in range(4):
         y, (want, slack) = product(handle, M, N, K, variant, 4, x)
         y = y.cpu()
         assert bool(torch.isnan(y[37]).all())
@@ -180,7 +180,7 @@ def test_refusals_write_nothing(handle):
         (lambda: sw.swiglu_forward_mxfp4(handle, q, s, q, s, y, 64, 12, 64), sw.ERR_UNSUPPORTED),
         (lambda: sw.swiglu_forward_mxfp4(handle, q, s, q, s, y, 64, 8, 48), sw.ERR_UNSUPPORTED),
         (lambda: sw.swiglu_forward_mxfp4(handle, q, s, q, s, q, 64, 8, 64), sw.ERR_INVALID_ARG),
-        (lambda: sw.swiglu_forward_mxfp4(handle, q, s, q, s, y, 64, 8, 64, variant=5),
+        (lambda: sw.swiglu_forward_mxfp4(handle, q, s, q, s, y, 64, 8, 64, variant=4),
          sw.ERR_INVALID_ARG),
     ]
     for call, status in cases:

@@ -136,7 +136,7 @@ def test_forward_mxfp4(handle):
     check("swiglu_forward_mxfp4", d, [
         (dict(h=None), INVALID), (dict(Q=None), INVALID), (dict(SQ=None), INVALID),
         (dict(W=None), INVALID), (dict(SW=None), INVALID), (dict(Y=None), INVALID),
-        (dict(M=-1), INVALID), (dict(N=-8), INVALID), (dict(K=-32), INVALID), (dict(variant=5), INVALID),
+        (dict(M=-1), INVALID), (dict(N=-8), INVALID), (dict(K=-32), INVALID), (dict(variant=4), INVALID),
         (dict(N=60), UNSUPPORTED), (dict(K=48), UNSUPPORTED), (dict(Y=P[4] + 8), UNSUPPORTED),
         (dict(Q=P[0] + 8), UNSUPPORTED), (dict(SW=P[3] + 8), UNSUPPORTED),
         (dict(K=(1 << 22) + 32), UNSUPPORTED), (dict(M=1 << 30), UNSUPPORTED),
