@@ -71,7 +71,7 @@ struct RouteArgs {
   int32_t* experts;
   int32_t* offsets;
   int32_t* rows;
-  int32_t* counts;  // workspace: [E, workgroups]
+  int32_t* counts;  // workspace: [workgroups, E rounded up to 4]
   int T, E, k, renorm;
   int vec;          // rows are 16-byte aligned and a multiple of 16 bytes
   int tokens;       // tokens of a workgroup
@@ -322,12 +322,13 @@ __global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a)
 }
 
 // ---- many tokens: choose and count, then place ---------------------------------------
-// The counts are [E, blocks] (rows of `stride` integers, a multiple of 4), so
-// that in the second launch one wave reads an expert's counts of all
-// workgroups with one 16-byte load a lane, all its experts' loads in flight
-// together (a loop over workgroups, a load each, took 34 us at 256 of them).
+// The counts are [blocks, stride], stride = E rounded up to 4: a thread of the
+// second launch adds up four experts' counts over every RP-th workgroup, eight
+// 16-byte loads in flight, and LDS adds up the threads.  (One wave an expert
+// with a scan over the workgroups took 1.1 us more at 128 experts and 8191
+// tokens, 3.0 at 200 and 2000.)
 constexpr int kSelectThreads = 512, kPlaceThreads = 1024;
-constexpr int kMaxRouteBlocks = 256;  // one 16-byte load of a wave
+constexpr int kMaxRouteBlocks = 256;  // one on every CU
 template <typename In, int G, int C>
 __global__ __launch_bounds__(kSelectThreads) void route_select_kernel(RouteArgs a, int stride) {
   __shared__ __attribute__((aligned(16))) int hist[G * C];
@@ -338,46 +339,64 @@ __global__ __launch_bounds__(kSelectThreads) void route_select_kernel(RouteArgs 
   route_tokens<In, G, C>(a, t0, min(t0 + a.tokens, a.T), picked, hist, nullptr);
   __syncthreads();
   for (int i = threadIdx.x; i < a.E; i += blockDim.x)
-    a.counts[(size_t)i * stride + blockIdx.x] = hist[i];
+    a.counts[(size_t)blockIdx.x * stride + i] = hist[i];
 }
 
 template <int EMAX>
 __global__ __launch_bounds__(kPlaceThreads) void route_place_kernel(RouteArgs a, int stride) {
-  constexpr int NW = kPlaceThreads / 64, PER = EMAX / NW;  // experts a wave
+  constexpr int NW = kPlaceThreads / 64;
+  constexpr int VP = EMAX / 4, RP = kPlaceThreads / VP;       // threads a row, rows at a time
+  constexpr int RG = kPlaceThreads / (VP < 64 ? 64 : VP);     // sums left to LDS
   __shared__ __attribute__((aligned(16))) int next[NW * EMAX];
+  __shared__ __attribute__((aligned(16))) u32x4 part[2 * RG * VP];
   __shared__ __attribute__((aligned(16))) int count[EMAX];
   __shared__ __attribute__((aligned(16))) int base[EMAX];
   __shared__ __attribute__((aligned(16))) int offset[EMAX + 1];
-  const int nb = gridDim.x, me = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  static_assert(VP >= 32 && (VP & (VP - 1)) == 0 && RP >= 1, "rows of half a wave or more");
+  const int nb = gridDim.x, me = blockIdx.x;
   const int s0 = me * a.tokens * a.k, s1 = min(s0 + a.tokens * a.k, a.T * a.k);
   const RouteShare share = route_share(a.experts, s0, s1);
   for (int i = threadIdx.x; i < NW * a.E; i += blockDim.x) next[i] = 0;
-  constexpr int STEP = PER < 8 ? PER : 8;  // loads in flight a lane
-  for (int j0 = 0; j0 < PER; j0 += STEP) {
-    u32x4 n[STEP];
+  // counts of all workgroups, and of those before this one
+  const int v = threadIdx.x % VP, r0 = threadIdx.x / VP;
+  u32x4 all{0, 0, 0, 0}, mine{0, 0, 0, 0};
+  for (int r = r0; r < nb; r += RP * 8) {
+    u32x4 n[8];
 #pragma unroll
-    for (int j = 0; j < STEP; ++j) {
-      const int x = wave + NW * (j0 + j);
-      n[j] = x < a.E && 4 * lane < nb ? load16(a.counts + (size_t)x * stride + 4 * lane)
-                                      : u32x4{0, 0, 0, 0};
-    }
+    for (int j = 0; j < 8; ++j)
+      n[j] = r + RP * j < nb && 4 * v < a.E
+                 ? load16(a.counts + (size_t)(r + RP * j) * stride + 4 * v)
+                 : u32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < STEP; ++j) {
-      int all = 0, mine = 0;
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int b = 4 * lane + q, v = b < nb ? (int)n[j][q] : 0;  // the last group's padding
-        all += v;
-        mine += b < me ? v : 0;
+        all[q] += n[j][q];
+        mine[q] += r + RP * j < me ? n[j][q] : 0;
       }
-      all = wave_scan(all);
-      mine = wave_scan(mine);
-      const int x = wave + NW * (j0 + j);
-      if (lane == 63 && x < a.E) count[x] = all, base[x] = mine;
+  }
+  if constexpr (VP == 32) {  // two rows a wave
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      all[q] += (uint32_t)__shfl_xor((int)all[q], 32);
+      mine[q] += (uint32_t)__shfl_xor((int)mine[q], 32);
     }
   }
+  const int group = threadIdx.x / (VP < 64 ? 64 : VP);
+  if (VP >= 64 || (threadIdx.x & 63) < 32) {
+    part[(2 * group) * VP + v] = all;
+    part[(2 * group + 1) * VP + v] = mine;
+  }
   __syncthreads();
+  const int* sums = reinterpret_cast<const int*>(part);
+  for (int x = threadIdx.x; x < 2 * EMAX; x += blockDim.x) {
+    int n = 0;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) n += sums[2 * g * EMAX + x];
+    (x < EMAX ? count : base)[x % EMAX] = n;
+  }
   route_count(a, a.experts, share, next);
+  __syncthreads();
   route_scan(count, offset, a.E);
   __syncthreads();
   route_bases<NW>(next, offset, base, a.E);
@@ -404,7 +423,7 @@ static int route_blocks(long long T, long long E, long long k, long long* tokens
 long long route_workspace_bytes(long long T, long long E, long long k) {
   if (T * k <= kRouteSmall) return 0;
   long long tokens;
-  return (route_blocks(T, E, k, &tokens) + 3LL) / 4 * 4 * E * 4;
+  return route_blocks(T, E, k, &tokens) * ((E + 3) / 4 * 4) * 4;
 }
 
 template <typename In, int G, int C>
@@ -415,7 +434,7 @@ static hipError_t launch_route_as(RouteArgs a, hipStream_t stream) {
     return launch_op(route_small_kernel<In, G, C>, dim3(1), dim3(threads), stream, a);
   }
   long long tokens;
-  const int blocks = route_blocks(a.T, a.E, a.k, &tokens), stride = (blocks + 3) / 4 * 4;
+  const int blocks = route_blocks(a.T, a.E, a.k, &tokens), stride = (a.E + 3) / 4 * 4;
   a.tokens = (int)tokens;
   const hipError_t e = launch_op(route_select_kernel<In, G, C>, dim3(blocks), dim3(kSelectThreads),
                                  stream, a, stride);
