@@ -59,9 +59,9 @@ __device__ __forceinline__ int group_a_row(const GroupArgs& g, int pos) {
 // sums are added in LDS at the end: twice the waves for a small tile.
 // Rows past the span, columns past the matrix and k past K arrive as zeros (a
 // buffer load past the resource returns 0).  Bound by the matrix pipes and the
-// power they draw: 32760 rows, 32 experts, 3584 x 4736 in 1010 to 1083 us (1.03 to
-// 1.10 PFLOP/s, 67 % of the cycles in the pipes at 1.35 GHz); 2368 x 3584 in 553
-// to 581 us.
+// power they draw: 32760 rows, 32 experts, 3584 x 4736 in 1010 to 1160 us from card
+// to card (0.96 to 1.10 PFLOP/s, 67 % of the cycles in the pipes at 1.35 GHz); 2368 x
+// 3584 in 553 to 624 us.
 template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int KG = 1>
 struct GroupTile {
   static constexpr int BK = 32 * KG;
@@ -376,98 +376,84 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void grouped_tile_kernel(Group
 // ============================================================================
 // Few rows an expert: weight streaming
 // ============================================================================
-// One workgroup takes up to 16 MT rows of one expert and a slab of 128 of its
+// One workgroup takes up to 16 rows of one expert and a slab of 128 of its
 // weight columns; its NW waves take every NW-th step of 32 k.  A lane loads an
 // 8 (k) x 8 (column) block of weights into registers, transposes it there and
-// feeds eight v_mfma_f32_16x16x32_bf16 per 16 rows; other waves' loads are in
-// flight meanwhile.  The waves' fp32 sums are added in LDS in wave order, so
-// the result does not depend on timing; up applies SiLU after that.  32 rows on
-// 64 experts, 1536 x 3584: 59.8 us, 5.9 TB/s of weights.
-template <int OP, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 2)))
+// feeds eight v_mfma_f32_16x16x32_bf16; other waves' loads are in flight
+// meanwhile.  The waves' fp32 sums are added in LDS in wave order, so the result
+// does not depend on timing; up applies SiLU after that.  32 rows on 64 experts,
+// 1536 x 3584: 59.8 us, 5.9 TB/s of weights.
+constexpr int kStreamRows = 16;
+template <int OP, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(4)))
 void grouped_stream_kernel(GroupArgs g, int nslab) {
-  __shared__ __attribute__((aligned(16))) f32x4 red[NW * MT * 8 * 64];
+  __shared__ __attribute__((aligned(16))) f32x4 red[NW * 8 * 64];
   const int x = blockIdx.x % 8;
-  const GroupRange range = group_range<16 * MT, 1>(g.offsets, g.E, g.R, nslab, x);
+  const GroupRange range = group_range<kStreamRows, 1>(g.offsets, g.E, g.R, nslab, x);
   const int t = range.begin + (int)blockIdx.x / 8;
   if (t >= range.end) return;
-  const GroupUnit u = group_unit<16 * MT>(g.offsets, g.E, g.R, nslab, t);
+  const GroupUnit u = group_unit<kStreamRows>(g.offsets, g.E, g.R, nslab, t);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int slab = u.local % nslab, pos0 = u.first + u.local / nslab * (16 * MT);
-  const int nrows = min(u.first + u.rows - pos0, 16 * MT);
+  const int slab = u.local % nslab, pos0 = u.first + u.local / nslab * kStreamRows;
+  const int nrows = min(u.first + u.rows - pos0, kStreamRows);
   const int K = g.K, ldw = g.ldw;
   const uint16_t* W = g.W + (size_t)u.expert * K * ldw;
   const int c0 = slab * 128 + (lane & 15) * 8;
   const bool cin = c0 < ldw;  // ldw % 8 == 0: eight columns are in range together
 
-  // this lane's row of A in each block of 16; rows past the span repeat the
-  // last one (an output row depends on its own row of A alone, and those are
-  // never stored)
-  const uint16_t* ap[MT];
-  bool ain[MT];
+  // this lane's row of A; rows past the span repeat the last one (an output row
+  // depends on its own row of A alone, and those are never stored)
+  const int ar = group_a_row<OP>(g, pos0 + min(lane & 15, nrows - 1));
+  const bool ain = ar >= 0;
+  const uint16_t* ap = g.A + (size_t)max(ar, 0) * K;
+  f32x4 acc[8];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int ar = group_a_row<OP>(g, pos0 + min(mt * 16 + (lane & 15), nrows - 1));
-    ain[mt] = ar >= 0;
-    ap[mt] = g.A + (size_t)max(ar, 0) * K;
-  }
-  f32x4 acc[MT][8];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[mt][c] = f32x4{};
+  for (int c = 0; c < 8; ++c) acc[c] = f32x4{};
 
   const int nsteps = (K + 31) / 32;
   for (int s = wave; s < nsteps; s += NW) {
     const int k = s * 32 + (lane >> 4) * 8;
     const bool kin = k < K;  // K % 8 == 0: eight k are in range together
-    u32x4 w[8], a[MT], col[8];
+    u32x4 w[8], col[8];
     const uint16_t* p = W + (size_t)k * ldw + c0;
 #pragma unroll
     for (int r = 0; r < 8; ++r)
       w[r] = kin && cin ? load16_stream(p + (size_t)r * ldw) : u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-      a[mt] = kin && ain[mt] ? load16(ap[mt] + k) : u32x4{0, 0, 0, 0};
+    const u32x4 a = kin && ain ? load16(ap + k) : u32x4{0, 0, 0, 0};
     transpose8x8(w, col);
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) acc[mt][c] = mfma16(a[mt], col[c], acc[mt][c]);
+    for (int c = 0; c < 8; ++c) acc[c] = mfma16(a, col[c], acc[c]);
   }
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) red[((wave * MT + mt) * 8 + c) * 64 + lane] = acc[mt][c];
+  for (int c = 0; c < 8; ++c) red[(wave * 8 + c) * 64 + lane] = acc[c];
   __syncthreads();
+  if (wave > 0) return;
 
   // register r of a lane is row 4 (lane / 16) + r, accumulator c column c0 + c
-  for (int mt = wave; mt < MT; mt += NW) {
-    f32x4 v[8];
+  f32x4 v[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      v[c] = red[(mt * 8 + c) * 64 + lane];
-      for (int w = 1; w < NW; ++w) v[c] += red[((w * MT + mt) * 8 + c) * 64 + lane];
-    }
-    if (!cin) continue;
+  for (int c = 0; c < 8; ++c) {
+    v[c] = red[c * 64 + lane];
+    for (int w = 1; w < NW; ++w) v[c] += red[(w * 8 + c) * 64 + lane];
+  }
+  if (!cin) return;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = mt * 16 + (lane >> 4) * 4 + r;
-      if (row >= nrows) continue;
-      const int out = OP == GROUP_UP ? pos0 + row : g.rows[pos0 + row];
-      if (out < 0 || out >= g.R) continue;
-      uint16_t* y = g.Y + (size_t)out * g.N;
-      if constexpr (OP == GROUP_UP) {
-        float s[4];
+  for (int r = 0; r < 4; ++r) {
+    const int row = (lane >> 4) * 4 + r;
+    if (row >= nrows) continue;
+    const int out = OP == GROUP_UP ? pos0 + row : g.rows[pos0 + row];
+    if (out < 0 || out >= g.R) continue;
+    uint16_t* y = g.Y + (size_t)out * g.N;
+    if constexpr (OP == GROUP_UP) {
+      float s[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] = silu(v[2 * q][r]) * v[2 * q + 1][r];
-        *reinterpret_cast<u32x2*>(y + c0 / 2) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
-      } else {
-        u32x4 o;
+      for (int q = 0; q < 4; ++q) s[q] = silu(v[2 * q][r]) * v[2 * q + 1][r];
+      *reinterpret_cast<u32x2*>(y + c0 / 2) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+    } else {
+      u32x4 o;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(v[2 * q][r], v[2 * q + 1][r]);
-        *reinterpret_cast<u32x4*>(y + c0) = o;
-      }
+      for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(v[2 * q][r], v[2 * q + 1][r]);
+      *reinterpret_cast<u32x4*>(y + c0) = o;
     }
   }
 }
@@ -497,21 +483,21 @@ static hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
   return launch_op(grouped_tile_kernel<OP, BM, BNW, STAGES, WGM, WGN, PARTS, PWGM, PWGN, KG>,
                    dim3((unsigned)grid), dim3(64 * WGM * WGN * KG), stream, g, (int)ntn);
 }
-template <int OP, int MT, int NW>
+template <int OP, int NW>
 static hipError_t launch_stream(const GroupArgs& g, hipStream_t stream) {
   const long long nslab = (g.ldw + 127) / 128;
   // one workgroup a unit: all units weigh the same, so no XCD has more than an
   // eighth of them, rounded up
-  const long long units = (max_row_tiles(g.R, g.E, 16 * MT) * nslab + 7) / 8 * 8;
+  const long long units = (max_row_tiles(g.R, g.E, kStreamRows) * nslab + 7) / 8 * 8;
   if (units > 0x7fffffffLL) return hipErrorInvalidValue;
-  return launch_op(grouped_stream_kernel<OP, MT, NW>, dim3((unsigned)units), dim3(64 * NW),
+  return launch_op(grouped_stream_kernel<OP, NW>, dim3((unsigned)units), dim3(64 * NW),
                    stream, g, (int)nslab);
 }
 
 template <int OP>
 static hipError_t launch_grouped_op(const GroupArgs& g, int variant, hipStream_t stream) {
   switch (variant) {
-    case 0: return launch_stream<OP, 1, 8>(g, stream);
+    case 0: return launch_stream<OP, 8>(g, stream);
     case 1: return launch_tile<OP, 64, 128, 4, 2, 2, 1, 2, 2>(g, stream);
     case 2: return launch_tile<OP, 128, 128, 4, 2, 2, 2, 2, 2>(g, stream);
     case 4: return launch_tile<OP, 64, 64, 4, 2, 1, 1, 2, 1, 2>(g, stream);
