@@ -16,7 +16,7 @@
 // does all of it in one launch; beyond that one launch chooses and counts, a
 // second one places.  The order comes from counts and ranks, never from the
 // arrival of atomics, so it is the same in every run.  8191 tokens, 128 experts, 8
-// choices: 4.8 us to choose, 5.4 to place, 10.0 a call; one token: 4.2 us.
+// choices: 4.8 us to choose, 5.4 to 6.0 to place, 10.0 a call; one token: 4.2 us.
 #include "swiglu_internal.h"
 #include "swiglu_ops_device.hpp"
 
