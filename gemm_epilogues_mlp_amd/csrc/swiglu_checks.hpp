@@ -116,7 +116,7 @@ inline int combine_norm(const NormCall& c, int dtype, bool* noop) {
   if (c.D % 8 != 0 || c.D > kMaxNormWidth || c.T > kMaxInt / 4 || c.k > kMaxInt ||
       mul(mul(c.T, c.k), 2 * c.D) > kMaxTotal || mul(c.T, 4 * c.D) > kMaxTotal)
     return kUnsupported;
-  if (c.gate && (c.gate_ld % 8 != 0 || mul(c.T, 2 * c.gate_ld) > kMaxTotal)) return kUnsupported;
+  if (c.gate && (c.gate_ld % 8 != 0 || mul(c.T, mul(2, c.gate_ld)) > kMaxTotal)) return kUnsupported;
   if (!aligned16({c.B, c.S, c.X, c.post, c.gate, c.pre, c.X_out, c.H}) || !aligned(c.weights, 4) ||
       !aligned(c.experts, 4))
     return kUnsupported;
