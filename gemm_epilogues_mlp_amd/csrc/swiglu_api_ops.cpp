@@ -26,7 +26,7 @@ swiglu_status_t run_grouped(swiglu_handle_t h, bool up, const void* A, const int
                             hipStream_t stream) {
   if (!h || variant >= kGroupedVariants) return SWIGLU_ERR_INVALID_ARG;
   bool noop;
-  const int c = checks::grouped(up, A, rows, offsets, W, Y, TA, R, N, K, E, k, &noop);
+  const int c = checks::grouped(up, A, rows, offsets, W, Y, TA, R, N, K, E, k, variant, &noop);
   if (c != checks::kOk || noop) return (swiglu_status_t)c;
   const swiglu_status_t st = check_device(h);
   if (st != SWIGLU_OK) return st;

@@ -18,6 +18,7 @@ constexpr long long kMaxInt = 0x7fffffffLL;
 constexpr long long kMax2G = 1LL << 31;
 constexpr long long kMaxSlots = 1LL << 30;
 constexpr long long kMaxTotal = 1LL << 46;  // bytes of a tensor addressed with 64 bits
+constexpr long long kMaxThreads = (1LL << 32) - 1;  // of a launch, along x
 
 struct Span {
   const void* p;
@@ -75,7 +76,7 @@ inline int route(const void* logits, const void* weights, const void* experts, c
 
 inline int grouped(bool up, const void* A, const void* rows, const void* offsets, const void* W,
                    const void* Y, long long TA, long long R, long long N, long long K, long long E,
-                   long long k, bool* noop) {
+                   long long k, int variant, bool* noop) {
   *noop = false;
   if (TA < 0 || R < 0 || N < 0 || K < 0 || E < 1 || k < 1) return kInvalid;
   if (R == 0 || N == 0) {
@@ -97,6 +98,7 @@ inline int grouped(bool up, const void* A, const void* rows, const void* offsets
   // expert, times the column tiles of 128
   const long long some = R < E ? R : E;
   if (mul(R / 16 + some + 1, ((up ? 2 : 1) * N + 127) / 128) > kMaxInt) return kUnsupported;
+  if (grouped_threads(up, R, N, E, variant) > kMaxThreads) return kUnsupported;
   if (clash({{Y, ybytes}},
             {{A, abytes}, {W, mul(E, wbytes)}, {rows, 4 * R}, {offsets, 4 * (E + 1)}}))
     return kInvalid;
@@ -116,6 +118,7 @@ inline int combine_norm(const NormCall& c, int dtype, bool* noop) {
   if (c.D % 8 != 0 || c.D > kMaxNormWidth || c.T > kMaxInt / 4 || c.k > kMaxInt ||
       mul(mul(c.T, c.k), 2 * c.D) > kMaxTotal || mul(c.T, 4 * c.D) > kMaxTotal)
     return kUnsupported;
+  if (norm_threads(c.T, c.D) > kMaxThreads) return kUnsupported;
   if (c.gate && (c.gate_ld % 8 != 0 || mul(c.T, mul(2, c.gate_ld)) > kMaxTotal)) return kUnsupported;
   if (!aligned16({c.B, c.S, c.X, c.post, c.gate, c.pre, c.X_out, c.H}) || !aligned(c.weights, 4) ||
       !aligned(c.experts, 4))
@@ -144,7 +147,7 @@ inline int convert_mxfp4(const void* X, const void* Q, const void* S, long long 
   if (K % 32 != 0 || rows > kMaxInt || K > kMaxInt || mul(rows + 31, 2 * (K + 255)) > kMaxTotal)
     return kUnsupported;
   const long long q = fp4_code_bytes(rows, K), s = fp4_scale_bytes(rows, K);
-  if (q / 1024 > kMaxInt - 16) return kUnsupported;  // one wave for each 1 KB of codes
+  if (q / 1024 * 64 > kMaxThreads) return kUnsupported;  // one wave for each 1 KB of codes
   if (!aligned16({X, Q, S})) return kUnsupported;
   const Span x{X, 2 * rows * K}, cq{Q, q}, cs{S, s};
   if (back ? clash({x}, {cq, cs}) : clash({cq, cs}, {x})) return kInvalid;
@@ -169,6 +172,9 @@ inline int forward_mxfp4(const Fp4Call& c, bool* noop) {
   const __int128 a128 = (__int128)((c.M + 31) / 32) * ((c.K + 255) / 256) * 4096;
   const __int128 w128 = (__int128)((2 * c.N + 31) / 32) * ((c.K + 255) / 256) * 4096;
   if (a128 >= kMax2G || w128 >= kMax2G || mul(c.M, 2 * c.N) > kMaxTotal) return kUnsupported;
+  // eight waves for each block of 32 weight rows where they are streamed (with
+  // K > 0 the weights' 2 GiB end sooner)
+  if ((2 * c.N + 31) / 32 * 512 > kMaxThreads) return kUnsupported;
   // tiles of 128 x 64 outputs, the smallest
   if (mul((c.M + 127) / 128, (c.N + 63) / 64) > kMaxInt) return kUnsupported;
   if (clash({{c.Y, 2 * c.M * c.N}},

@@ -468,29 +468,36 @@ static long long max_row_tiles(long long R, long long E, long long bm) {
   return std::min(R, (R + some * (bm - 1)) / bm);
 }
 
+// Workgroups of the tile kernel.  Every XCD's range needs workgroups there.  With
+// short tiles an eighth of the work can be up to 2.2 eighths of the units; while
+// the launch is about a round of workgroups, the extra ones cost nothing and a
+// second unit in turn would double the time, beyond that the loop takes what is
+// left over.
+static long long tile_grid(long long R, long long E, long long ldw, int bm, int bnw, int parts) {
+  const long long units = max_row_tiles(R, E, bm) * ((ldw + bnw - 1) / bnw);
+  return (units * (parts > 1 && units < 1024 ? 2 : 1) + 7) / 8 * 8;
+}
+// Of the streaming kernel: one a unit.  All units weigh the same, so no XCD has
+// more than an eighth of them, rounded up.
+static long long stream_grid(long long R, long long E, long long ldw) {
+  return (max_row_tiles(R, E, kStreamRows) * ((ldw + 127) / 128) + 7) / 8 * 8;
+}
+
 template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN,
           int KG = 1>
 static hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
   static_assert(WGM * WGN == PWGM * PWGN && (PARTS == 1 || PARTS == 2 || PARTS == 4), "one workgroup");
   const long long ntn = (g.ldw + BNW - 1) / BNW;
-  // Every XCD's range needs workgroups there.  With short tiles an eighth of
-  // the work can be up to 2.2 eighths of the units; while the launch is about
-  // a round of workgroups, the extra ones cost nothing and a second unit in
-  // turn would double the time, beyond that the loop takes what is left over.
-  const long long units = max_row_tiles(g.R, g.E, BM) * ntn;
-  const long long grid = (units * (PARTS > 1 && units < 1024 ? 2 : 1) + 7) / 8 * 8;
+  const long long grid = tile_grid(g.R, g.E, g.ldw, BM, BNW, PARTS);
   if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
   return launch_op(grouped_tile_kernel<OP, BM, BNW, STAGES, WGM, WGN, PARTS, PWGM, PWGN, KG>,
                    dim3((unsigned)grid), dim3(64 * WGM * WGN * KG), stream, g, (int)ntn);
 }
 template <int OP, int NW>
 static hipError_t launch_stream(const GroupArgs& g, hipStream_t stream) {
-  const long long nslab = (g.ldw + 127) / 128;
-  // one workgroup a unit: all units weigh the same, so no XCD has more than an
-  // eighth of them, rounded up
-  const long long units = (max_row_tiles(g.R, g.E, kStreamRows) * nslab + 7) / 8 * 8;
-  if (units > 0x7fffffffLL) return hipErrorInvalidValue;
-  return launch_op(grouped_stream_kernel<OP, NW>, dim3((unsigned)units), dim3(64 * NW),
+  const long long nslab = (g.ldw + 127) / 128, grid = stream_grid(g.R, g.E, g.ldw);
+  if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
+  return launch_op(grouped_stream_kernel<OP, NW>, dim3((unsigned)grid), dim3(64 * NW),
                    stream, g, (int)nslab);
 }
 
@@ -526,6 +533,19 @@ static int grouped_variant(long long R, long long E, long long ldw) {
   if (wide >= 200 && mean <= 10) return 0;
   if (wide >= 200 && mean <= 28) return 1;
   return 3;
+}
+
+// Threads of the launch that launch_grouped_op makes.
+long long grouped_threads(bool up, long long R, long long N, long long E, int variant) {
+  const long long ldw = up ? 2 * N : N;
+  if (variant < 0) variant = grouped_variant(R, E, ldw);
+  switch (variant) {
+    case 0: return stream_grid(R, E, ldw) * 512;
+    case 1: return tile_grid(R, E, ldw, 64, 128, 1) * 256;
+    case 2: return tile_grid(R, E, ldw, 128, 128, 2) * 256;
+    case 4: return tile_grid(R, E, ldw, 64, 64, 1) * 256;
+    default: return tile_grid(R, E, ldw, 256, 256, 4) * 512;
+  }
 }
 
 hipError_t launch_grouped(bool up, const uint16_t* A, const int32_t* rows, const int32_t* offsets,

@@ -120,6 +120,7 @@ hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* e
                         bool renorm, hipStream_t stream);
 // Grouped products; TA: rows of A, variant < 0: by rule
 constexpr int kGroupedVariants = 5;
+long long grouped_threads(bool up, long long R, long long N, long long E, int variant);
 hipError_t launch_grouped(bool up, const uint16_t* A, const int32_t* rows, const int32_t* offsets,
                           const uint16_t* W, uint16_t* Y, int TA, int R, int N, int K, int E,
                           int k, int variant, hipStream_t stream);
@@ -134,6 +135,7 @@ struct NormCall {
   long long gate_ld;
   bool f32;  // X and X_out
 };
+long long norm_threads(long long T, long long D);
 hipError_t launch_combine_norm(const NormCall& c, hipStream_t stream);
 
 // ---- MXFP4 (swiglu_fp4.hip) ----------------------------------------------------

@@ -238,6 +238,13 @@ static hipError_t launch_norm_x(const NormArgs& a, hipStream_t stream) {
   return launch_norm_as<XF32, 16, 2>(a, stream);
 }
 
+// Threads of the launch: a wave a token for many narrow ones, else the waves
+// of launch_norm_x for each token.
+long long norm_threads(long long T, long long D) {
+  if (D <= 2048) return T >= 1024 ? (T + 3) / 4 * 256 : T * 256;
+  return T * (D <= 8192 ? 512 : 1024);
+}
+
 hipError_t launch_combine_norm(const NormCall& c, hipStream_t stream) {
   const NormArgs a{(const uint16_t*)c.B,    c.weights, c.experts, (const uint16_t*)c.S,
                    c.X,                     (const uint16_t*)c.post, (const uint16_t*)c.gate,

@@ -513,7 +513,8 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
  * below that.  bf16 tensors, fp32 sums, one rounding.
  * N % 8 == 0, K % 8 == 0, N <= 2^23, 16-byte aligned tensors, A and one
  * expert's weights under 2 GiB, E <= 1024 (else UNSUPPORTED); all of W and Y may
- * be larger.
+ * be larger, up to a launch of 2^32 threads (also UNSUPPORTED; with N < 2^18 not
+ * before Y has 8 GiB).
  * variant < 0: the kernel is chosen from R, E and N; 0 ... 4 force one (tests
  * and tuning), a larger one is INVALID_ARG. */
 swiglu_status_t swiglu_grouped_forward(swiglu_handle_t h, const void* A, const int32_t* rows,
@@ -540,8 +541,9 @@ swiglu_status_t swiglu_grouped_matmul(swiglu_handle_t h, const void* A, const in
  * B [T k, D], S, post, gate, pre and H are bf16, X and X_out of dtype, weights
  * fp32 and experts int32 [T, k]; arithmetic is fp32.  k = 0 leaves the sum to
  * S.  X_out may be X itself, else no output may overlap an input or the other
- * (INVALID_ARG).  D % 8 == 0, D <= 16384, gate_ld % 8 == 0 and 16-byte aligned
- * tensors (else UNSUPPORTED). */
+ * (INVALID_ARG).  D % 8 == 0, D <= 16384, gate_ld % 8 == 0, 16-byte aligned
+ * tensors and a launch of fewer than 2^32 threads: T <= 2^26 - 4 for D <= 2048,
+ * < 2^23 for D <= 8192, else < 2^22 (else UNSUPPORTED). */
 swiglu_status_t swiglu_combine_norm(swiglu_handle_t h, const void* B, const float* weights,
                                     const int32_t* experts, const void* S, const void* X,
                                     const void* post, const void* gate, const void* pre,
@@ -570,19 +572,21 @@ int64_t swiglu_mxfp4_scale_bytes(int64_t rows, int64_t K);
  * floor(log2 max |x|) - 2 held to [-127, 127] (zeros and subnormals: -127; an
  * infinity counts as 2^128), elements x 2^-shared to the nearest value, the
  * even code at a tie, saturating at 6, the sign of zero kept.  A block with a
- * NaN gets byte 255 and unspecified codes.  K % 32 == 0 and 16-byte aligned
- * tensors (else UNSUPPORTED); outputs must not overlap X or each other. */
+ * NaN gets byte 255 and unspecified codes.  K % 32 == 0, 16-byte aligned tensors
+ * and codes under 64 GiB (else UNSUPPORTED); outputs must not overlap X or each
+ * other. */
 swiglu_status_t swiglu_quantize_mxfp4(swiglu_handle_t h, const void* X, void* Q, void* S,
                                       int64_t rows, int64_t K, hipStream_t stream);
 
 /* bf16 X [rows, K] from its codes, exact but for magnitudes from 2^128 on,
- * which become infinities; NaN where the block's byte is 255. */
+ * which become infinities; NaN where the block's byte is 255.  Limits as
+ * swiglu_quantize_mxfp4. */
 swiglu_status_t swiglu_dequantize_mxfp4(swiglu_handle_t h, const void* Q, const void* S, void* X,
                                         int64_t rows, int64_t K, hipStream_t stream);
 
 /* Y = bf16(SiLU(g) * u), g and u the Gate and Up products of activations
  * (Q, SQ) [M, K] and weights (W, SW) [2N, K] in MXFP4; exact products, fp32
- * sums.  N % 8 == 0, K % 32 == 0, K <= 2^22, 16-byte aligned tensors, the codes
+ * sums.  N % 8 == 0, N < 2^27, K % 32 == 0, K <= 2^22, 16-byte aligned tensors, the codes
  * of each under 2 GiB (else UNSUPPORTED); Y [M, N] must not overlap an input.
  * variant < 0: chosen from M and N; 0 ... 3 force one (tests and tuning). */
 swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const void* SQ,

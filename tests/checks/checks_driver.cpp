@@ -10,7 +10,12 @@
 #include "swiglu_checks.hpp"
 
 namespace swiglu {
+// stand-ins of the kernels' files, as large as theirs
 long long route_workspace_bytes(long long T, long long E, long long k) { return T * k > 512 ? 4 * E : 0; }
+long long grouped_threads(bool up, long long R, long long N, long long E, int) {
+  return (R / 16 + E) * ((up ? 2 : 1) * N / 64 + 1) * 512;
+}
+long long norm_threads(long long T, long long) { return T * 1024; }
 }  // namespace swiglu
 
 using namespace swiglu;
@@ -44,7 +49,7 @@ int main() {
   });
   for (bool up : {false, true})
     sweep("grouped", {10, 20, 64, 40, 8, 2}, [&](const std::vector<long long>& s) {
-      return checks::grouped(up, at(0), at(1), at(2), at(3), at(4), s[0], s[1], s[2], s[3], s[4], s[5], &noop);
+      return checks::grouped(up, at(0), at(1), at(2), at(3), at(4), s[0], s[1], s[2], s[3], s[4], s[5], -1, &noop);
     });
   for (int dtype : {0, 1})
     sweep("combine_norm", {10, 64, 2, 64}, [&](const std::vector<long long>& s) {
