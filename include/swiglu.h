@@ -513,8 +513,8 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
  * below that.  bf16 tensors, fp32 sums, one rounding.
  * N % 8 == 0, K % 8 == 0, N <= 2^23, 16-byte aligned tensors, A and one
  * expert's weights under 2 GiB, E <= 1024 (else UNSUPPORTED); all of W and Y may
- * be larger, up to a launch of 2^32 threads (also UNSUPPORTED; with N < 2^18 not
- * before Y has 8 GiB).
+ * be larger, up to a launch of 2^32 threads (also UNSUPPORTED; the streaming
+ * variant 0 takes 512 for every 16 rows of an expert and 128 columns of W).
  * variant < 0: the kernel is chosen from R, E and N; 0 ... 4 force one (tests
  * and tuning), a larger one is INVALID_ARG. */
 swiglu_status_t swiglu_grouped_forward(swiglu_handle_t h, const void* A, const int32_t* rows,
