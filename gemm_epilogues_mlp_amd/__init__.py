@@ -160,20 +160,13 @@ def _ptr(x) -> int | None:
         raise
 
 
-_torch_c = None  # torch._C, once torch has set the device up
-
-
 def _stream(stream) -> int | None:
     if stream is None:
         # torch's current stream as a plain handle: torch.cuda.current_stream()
-        # builds a Stream object first, 2.9 of a small call's 6.5 us
-        global _torch_c
-        if _torch_c is None:
-            import torch
-            if not torch.cuda.is_initialized():
-                return torch.cuda.current_stream().cuda_stream
-            _torch_c = torch._C
-        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+        # builds a Stream object first, 2.9 of a small call's 6.5 us.  As there,
+        # current_device() sets the device up and raises in a forked child.
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

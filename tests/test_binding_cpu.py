@@ -1,0 +1,30 @@
+"""The binding's argument helpers, without a GPU: which stream a call without one
+takes, and what passes as an address."""
+import pytest
+import torch
+
+import gemm_epilogues_mlp_amd as sw
+
+
+@pytest.fixture
+def initialised(monkeypatch):
+    """torch as it is once the device is set up, current stream 1234 of device 3."""
+    monkeypatch.setattr(torch.cuda, "_initialized", True)
+    monkeypatch.setattr(torch.cuda, "_is_in_bad_fork", lambda: False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1231 + device,
+                        raising=False)
+
+
+def test_stream_is_torchs_current_one(initialised):
+    assert sw._stream(None) == 1234
+    assert sw._stream(77) == 77 and sw._stream(0) == 0
+
+
+def test_forked_child_is_refused(initialised, monkeypatch):
+    """A child forked after the device was set up must not launch on the parent's streams:
+    torch's own error, also where the parent has made calls before."""
+    assert sw._stream(None) == 1234
+    monkeypatch.setattr(torch.cuda, "_is_in_bad_fork", lambda: True)
+    with pytest.raises(RuntimeError, match="forked subprocess"):
+        sw._stream(None)
