@@ -164,9 +164,13 @@ def _stream(stream) -> int | None:
     if stream is None:
         # torch's current stream as a plain handle: torch.cuda.current_stream()
         # builds a Stream object first, 2.9 of a small call's 6.5 us.  As there,
-        # current_device() sets the device up and raises in a forked child.
+        # current_device() sets the device up and raises in a forked child.  The
+        # raw handle has no public name; a torch without it takes the Stream.
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

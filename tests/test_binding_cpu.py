@@ -28,3 +28,12 @@ def test_forked_child_is_refused(initialised, monkeypatch):
     monkeypatch.setattr(torch.cuda, "_is_in_bad_fork", lambda: True)
     with pytest.raises(RuntimeError, match="forked subprocess"):
         sw._stream(None)
+
+
+def test_torch_without_the_raw_handle(initialised, monkeypatch):
+    """A torch build that lacks the raw handle's private name: the public stream serves."""
+    class Stream:
+        cuda_stream = 4321
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
+    assert sw._stream(None) == 4321
