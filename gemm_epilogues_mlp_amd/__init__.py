@@ -152,12 +152,9 @@ def _ptr(x) -> int | None:
     """Device pointer of a tensor (data_ptr), an int address, or None."""
     if x is None:
         return None
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        if isinstance(x, int):
-            return x
-        raise
+    if isinstance(x, int):
+        return x
+    return x.data_ptr()
 
 
 def _stream(stream) -> int | None:

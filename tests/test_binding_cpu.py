@@ -37,3 +37,16 @@ def test_torch_without_the_raw_handle(initialised, monkeypatch):
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
     assert sw._stream(None) == 4321
+
+
+def test_an_address_is_taken_as_it_is():
+    """Addresses are told apart by type, before anything is asked of them (an exception a
+    pointer made calls with plain addresses 0.3 us slower for each)."""
+    class Address(int):
+        def __getattr__(self, name):
+            pytest.fail(f"asked for {name}")
+    assert sw._ptr(Address(4096)) == 4096 and sw._ptr(0) == 0 and sw._ptr(None) is None
+    t = torch.zeros(4)
+    assert sw._ptr(t) == t.data_ptr()
+    with pytest.raises(AttributeError):
+        sw._ptr("4096")
