@@ -54,14 +54,16 @@ __device__ __forceinline__ int group_a_row(const GroupArgs& g, int pos) {
 // straight into a ring of STAGES LDS buffers, STAGES - 1 steps ahead of the
 // matrix instructions, with one barrier a step; weight fragments are read with
 // the transposing LDS read, activation fragments with 16-byte reads, both from
-// XOR-swizzled chunks so that the lanes served together hit distinct banks.
+// XOR-swizzled chunks that spread the lanes served together over the banks (3 to
+// 4 % of the LDS-active cycles still conflict, by the counters).
 // With KG = 2 a step is 64 k, 32 of them for each of two groups of waves, whose
 // sums are added in LDS at the end: twice the waves for a small tile.
 // Rows past the span, columns past the matrix and k past K arrive as zeros (a
-// buffer load past the resource returns 0).  Bound by the matrix pipes and the
-// power they draw: 32760 rows, 32 experts, 3584 x 4736 in 1010 to 1160 us from card
-// to card (0.96 to 1.10 PFLOP/s, 67 % of the cycles in the pipes at 1.35 GHz); 2368 x
-// 3584 in 553 to 624 us.
+// buffer load past the resource returns 0).  32760 rows, 32 experts: 3584 x 4736 in
+// 997 to 1160 us from card to card (0.96 to 1.12 PFLOP/s), bound by the matrix pipes
+// and the power they draw (67 % of the cycles in the pipes at 1.35 GHz in a run of
+// 1236 us under the counters); 2368 x 3584 in 527 to 624 us, where the fill of each
+// tile's ring and the last round weigh more (53 % at 1.74 GHz in a run of 590 us).
 template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int KG = 1>
 struct GroupTile {
   static constexpr int BK = 32 * KG;
@@ -469,10 +471,13 @@ static long long max_row_tiles(long long R, long long E, long long bm) {
 }
 
 // Workgroups of the tile kernel.  Every XCD's range needs workgroups there.  With
-// short tiles an eighth of the work can be up to 2.2 eighths of the units; while
-// the launch is about a round of workgroups, the extra ones cost nothing and a
-// second unit in turn would double the time, beyond that the loop takes what is
-// left over.
+// short tiles an eighth of the work can be up to 2.2 eighths of the units, so up
+// to some rounds of workgroups there are twice as many as units; beyond that the
+// loop takes what is left over.  Measured (us, twice as many / as many; K = 1536):
+// tiles of 128 x 128, 8 experts of 513 rows and 60 of one, 400 units 39.4 / 48.5,
+// 800 67.3 / 67.5; tiles of 256 x 256, 16 experts of 257 and 16 of one, 288 units
+// 66.3 / 78.7; 8 of 1025 and 40 of one, 320 units 63.0 / 69.8, 640 119.1 / 110.7.
+// Evenly filled experts are level (658 units 121.1 / 120.0; 1092 174.1 / 170.0).
 static long long tile_grid(long long R, long long E, long long ldw, int bm, int bnw, int parts) {
   const long long units = max_row_tiles(R, E, bm) * ((ldw + bnw - 1) / bnw);
   return (units * (parts > 1 && units < 1024 ? 2 : 1) + 7) / 8 * 8;
@@ -513,7 +518,7 @@ static hipError_t launch_grouped_op(const GroupArgs& g, int variant, hipStream_t
 }
 
 // The counts are on the device; the mean rows of an expert decide, and whether
-// there is a workgroup for every CU.  Measured (us, 2048 x 2816 weights, 32
+// there is a workgroup for every CU.  Measured at many units (us, 2048 x 2816 weights, 32
 // experts, variants 0 / 1 / 3): mean 8: 61 / 70 / 75, 24: 114 / 72 / 78, 64: 244
 // / 93 / 80.  With few units the wide tiles stream better (8 experts, 3584 x
 // 4736, mean 8, 0 / 3: 57 / 52).  Where even those leave CUs idle the bytes that
@@ -522,7 +527,14 @@ static hipError_t launch_grouped_op(const GroupArgs& g, int variant, hipStream_t
 // variants 1 / 2 / 4 take 44.9 / 35.8 / 43.4 us with 168 tiles of 128 x 128 (4
 // experts, 3416 x 816, mean 644), 24.9 / 31.7 / 27.9 with 112 of them (3584 x
 // 1792, mean 250), and 22.7 / 29.4 / 14.7 with 84 of 64 x 128 (3584 x 896, mean
-// 150).
+// 150).  One row an expert (a single token), weights from HBM, variants 0 / 2 / 3 / 4,
+// the rule's choice in brackets: 1536 x 3584, 4 experts 14.6 / 17.4 / 22.2 / [13.4], 8
+// experts 18.5 / [19.7] / 24.4 / 22.8, 24 experts [48.7] / 56.6 / 60.6 / 58.1; 1792 x
+// 1536, 8 experts 15.9 / 19.0 / 24.8 / [14.1], 16 experts 19.0 / [21.6] / 27.3 / 24.6;
+// 3584 x 4736, 4 experts 27.0 / [38.7] / 45.8 / 33.6, 8 experts 55.6 / 54.8 / [50.1] /
+// 58.2.  So with so few rows and fewer than 128 wide tiles streaming is up to 30 %
+// faster than variant 2 that the rule takes, and between 128 and 200 of them than
+// variant 3 (32 rows on 16 of 64 experts, 1792 x 1536: 19.3 / 21.6 / [27.4] / 24.8).
 static int grouped_variant(long long R, long long E, long long ldw) {
   const long long some = std::min(R, E), mean = (R + E - 1) / E;
   auto units = [&](long long bm, long long bnw) {

@@ -13,9 +13,10 @@
 // its rounding); each input is read once, so the memory bounds it.
 //
 // A token's D values stay in registers: NW waves of it, VPL vectors of 8 a
-// lane.  Many tokens: one wave each (no barrier, k VPL 16-byte loads in flight
-// a lane); few tokens: as many waves as D has, for latency.  8191 tokens, 8 slots,
-// width 1536, fp32 stream: 66 us, 5.3 TB/s; one token, 6 slots, width 3584: 3.6 us.
+// lane.  Many narrow tokens: one wave each (no barrier, k VPL 16-byte loads in
+// flight a lane); else as many waves as D has (launch_norm_x has both sides).
+// 8191 tokens, 8 slots, width 1536, fp32 stream: 66 us, 5.3 TB/s; one token, 6
+// slots, width 3584: 3.5 us.
 #include "swiglu_internal.h"
 #include "swiglu_ops_device.hpp"
 
@@ -223,6 +224,13 @@ static hipError_t launch_norm_as(const NormArgs& a, hipStream_t stream) {
                    dim3(NW == 1 ? 256 : 64 * NW), stream, a);
 }
 
+// One wave a token from 1024 tokens and up to 2048 wide.  Measured (us, one wave /
+// several; 8 slots, shared row, bf16 stream): width 512: 256 tokens 4.4 / 4.6,
+// 1024 5.5 / 6.9, 8191 20.0 / 25.7; 1024: 1024 tokens 8.3 / 8.3, 8191 38.4 / 37.5;
+// 1536: 256 tokens 8.7 / 5.1, 1024 11.1 / 9.5, 8191 57.2 / 53.7; 2048: 256 tokens
+// 10.1 / 5.4, 1024 13.7 / 11.1, 16384 142.2 / 141.9.  The bound on tokens is right,
+// that on the width is late: from 1024 on one wave gains nothing, and at 1536 and
+// 2048 it loses 3 to 7 % of a long call and a fifth of one of 1024 tokens.
 template <bool XF32>
 static hipError_t launch_norm_x(const NormArgs& a, hipStream_t stream) {
   const int nv = a.D / 8;  // at most 2048

@@ -16,7 +16,8 @@
 // does all of it in one launch; beyond that one launch chooses and counts, a
 // second one places.  The order comes from counts and ranks, never from the
 // arrival of atomics, so it is the same in every run.  8191 tokens, 128 experts, 8
-// choices: 4.8 us to choose, 5.4 to 6.0 to place, 10.0 a call; one token: 4.2 us.
+// choices of bf16 logits: 4.8 to 5.1 us to choose, 5.4 to 6.2 to place, 10.0 to
+// 10.9 a call (fp32: 6.0 to 6.8 and 5.6 to 6.8, 10.9 to 12.2 a call); one token: 4.2 us.
 #include "swiglu_internal.h"
 #include "swiglu_ops_device.hpp"
 
@@ -129,7 +130,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, bool in, 
 // The same for bf16 logits.  A logit and its index fit one whole number, the
 // value's bits made monotone over 1023 - index, so the maximum alone names the
 // winner: no vote, no note, about half the operations a choice (the launch that
-// chooses: 5.7 us without, 4.6 us with them, at 8191 tokens, 128 experts, 8 choices).
+// chooses, timed in turn: 5.7 us without, 4.6 us with them, at 8191 tokens, 128
+// experts, 8 choices).
 // 0 is a closed place; every open logit's number is above it.
 __device__ __forceinline__ uint32_t route_key(float x, int index) {
   const uint32_t b = __builtin_bit_cast(uint32_t, x == 0.0f ? 0.0f : x);  // one zero
@@ -292,8 +294,12 @@ __device__ __forceinline__ void route_bases(int* next, const int* offset, const 
   }
 }
 
-// Slots that one workgroup still takes by itself: below this a second launch
-// costs more than the other workgroups' help gives.
+// Slots that one workgroup still takes by itself.  Measured (us of GPU time, one
+// launch / two): bf16, 64 experts, 8 choices: 256 slots 4.6 / 6.8, 512 6.4 / 7.0,
+// 768 8.8 / 7.0; fp32, whose choices take longer: 64 experts, 6 choices: 252 7.0 /
+// 7.3, 510 9.1 / 7.4; 256 experts, 8 choices: 128 6.3 / 8.4, 256 9.3 / 8.6, 512
+// 15.2 / 8.8.  So the bound is right for bf16, up to 512 slots late for fp32; a
+// second launch also adds 1 to 2 us of the caller's time.
 constexpr long long kRouteSmall = 512;
 
 // ---- one workgroup does everything -------------------------------------------------
