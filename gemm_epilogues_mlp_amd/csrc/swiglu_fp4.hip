@@ -434,7 +434,8 @@ static hipError_t launch_f4_tile(const Fp4Call& c, hipStream_t stream) {
   if (ntm * ntn > 0x7fffffffLL) return hipErrorInvalidValue;
   const int group_m = (int)std::min(ntm, 4LL);
   const int per_cu = C::LDS_BYTES <= 80 * 1024 ? 2 : 1;
-  const long long wgs = std::min<long long>(ntm * ntn, (long long)c.cu_count * per_cu);
+  // eight at least: each XCD's range of tiles needs a workgroup there
+  const long long wgs = std::min<long long>(ntm * ntn, std::max<long long>((long long)c.cu_count * per_cu, 8));
   return launch_op(fp4_tile_kernel<BM, BNW, WGM, WGN>, dim3((unsigned)wgs), dim3(C::kThreads),
                    stream, c.A, c.SA, c.W, c.SW, c.Y, (int)c.M, (int)c.N, (int)c.K, group_m);
 }

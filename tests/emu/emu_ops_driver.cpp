@@ -7,7 +7,9 @@
 //        emu_ops_driver [--plant P] [--cus C]  fp4 VARIANT M N K
 //        emu_ops_driver                        convert ROWS K
 // UP 1: gated products, 0: down; DROP: slots behind the spans; --grid: workgroups
-// of the tile kernel; --cus: compute units that the MXFP4 launch is told.
+// of the tile kernel; --cus: compute units that the MXFP4 launch is told.  The
+// products' values mean nothing here, but every element of Y that a launch has to
+// write must have been written, and no other one.
 #include <stdio.h>
 #include <stdlib.h>
 
@@ -77,6 +79,22 @@ T* alloc(size_t n) {
   return p;
 }
 
+constexpr uint16_t kUnwritten = 0xabab;
+uint16_t* alloc_y(size_t n) {
+  uint16_t* y = alloc<uint16_t>(n);
+  for (size_t i = 0; i < n; ++i) y[i] = kUnwritten;
+  return y;
+}
+void check_written(const uint16_t* y, size_t n, bool want) {
+  size_t bad = 0, first = 0;
+  for (size_t i = 0; i < n; ++i)
+    if ((y[i] != kUnwritten) != want && bad++ == 0) first = i;
+  if (!bad) return;
+  ++g_errors;
+  fprintf(stderr, "OUTPUT: %zu of %zu elements %s, the first is %zu\n", bad, n,
+          want ? "not written" : "written past the spans", first);
+}
+
 // the tile kernels of launch_grouped_op, with a grid of the caller's
 template <int OP, int BM, int BNW, int STAGES, int WGM, int WGN, int PARTS, int PWGM, int PWGN, int KG>
 void run_tiles(const swiglu::GroupArgs& g, int grid) {
@@ -104,7 +122,7 @@ void run_grouped(bool up, int variant, int N, int K, int k, int drop, const char
   for (int i = 0; i < R; ++i) rows[i] = i < n ? (int)((long long)i * 7919 % n) : -1;
   const uint16_t* A = alloc<uint16_t>((size_t)T * K);
   const uint16_t* W = alloc<uint16_t>((size_t)E * K * N * (up ? 2 : 1));
-  uint16_t* Y = alloc<uint16_t>((size_t)R * N);
+  uint16_t* Y = alloc_y((size_t)R * N);
   if (grid == 0) {
     swiglu::launch_grouped(up, A, rows, offsets, W, Y, T, R, N, K, E, up ? k : 1, variant, nullptr);
   } else {
@@ -112,14 +130,18 @@ void run_grouped(bool up, int variant, int N, int K, int k, int drop, const char
     if (up) run_few<swiglu::GROUP_UP>(g, variant, grid);
     else run_few<swiglu::GROUP_DOWN>(g, variant, grid);
   }
+  check_written(Y, (size_t)n * N, true);
+  check_written(Y + (size_t)n * N, (size_t)drop * N, false);
 }
 
 void run_fp4(int variant, int M, int N, int K, int cus) {
   using namespace swiglu;
+  uint16_t* Y = alloc_y((size_t)M * N);
   const Fp4Call c{alloc<uint8_t>(fp4_code_bytes(M, K)),     alloc<uint8_t>(fp4_scale_bytes(M, K)),
                   alloc<uint8_t>(fp4_code_bytes(2 * N, K)), alloc<uint8_t>(fp4_scale_bytes(2 * N, K)),
-                  alloc<uint16_t>((size_t)M * N),           M, N, K, cus};
+                  Y, M, N, K, cus};
   launch_forward_mxfp4(c, variant, nullptr);
+  check_written(Y, (size_t)M * N, true);
 }
 
 void run_convert(int rows, int K) {

@@ -22,6 +22,8 @@ WALKS = [("--grid", 8, "grouped", up, v, 264, k, 3, 5, "300,1,0,600,140,70") for
          for v in range(1, 5) for k in (8, 136, 320)]
 FP4 = [("fp4", v, m, n, k) for v in range(4) for m, n, k in ((1, 8, 32), (70, 72, 96), (300, 136, 544))]
 TILES = [("--cus", 8, "fp4", v, 900, 648, k) for v in (2, 3) for k in (32, 288, 768, 1056)]
+# a device of fewer CUs than the eight ranges that the tiles are dealt out in
+FEW = [("--cus", c, "fp4", v, 900, 648, 288) for v in (2, 3) for c in (1, 3, 7)]
 CONVERT = [("convert", rows, k) for rows, k in ((1, 32), (33, 288), (100, 896))]
 WALK = ("--grid", 8, "grouped", 1)
 SPANS = (264, 136, 3, 5, "300,1,0,600,140,70")
@@ -47,7 +49,7 @@ def runs(tmp_path_factory):
         r = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=300, env=env)
         return r.returncode, r.stdout + r.stderr
     with cf.ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
-        jobs = GROUPED + WALKS + FP4 + TILES + CONVERT + [p for p, _ in PLANTED]
+        jobs = GROUPED + WALKS + FP4 + TILES + FEW + CONVERT + [p for p, _ in PLANTED]
         yield dict(zip(jobs, ex.map(run, jobs)))
 
 
@@ -71,6 +73,10 @@ def test_mxfp4_products(runs):
 
 def test_mxfp4_workgroups_walk_over_tiles(runs):
     clean(runs, TILES)
+
+
+def test_mxfp4_on_few_compute_units(runs):
+    clean(runs, FEW)
 
 
 def test_mxfp4_conversions(runs):
