@@ -34,6 +34,9 @@ __all__ = [
     "swiglu_grouped_forward", "swiglu_grouped_matmul", "swiglu_combine_norm",
     "swiglu_mxfp4_bytes", "swiglu_mxfp4_scale_bytes", "swiglu_quantize_mxfp4",
     "swiglu_dequantize_mxfp4", "swiglu_forward_mxfp4",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "swiglu_route_scored", "swiglu_int8_packed_bytes",
+    "swiglu_pack_int8_fragments", "swiglu_quantize_int8", "swiglu_forward_int8",
+    "swiglu_matmul_int8", "swiglu_grouped_forward_int8", "swiglu_grouped_matmul_int8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -45,6 +48,7 @@ VARIANT_AUTO, VARIANT_SYNC, VARIANT_INTERLEAVE, VARIANT_GEMM, VARIANT_FP8, VARIA
     VARIANT_MXFP8, VARIANT_PACKED, VARIANT_FP8_PACKED, VARIANT_MXFP8_PACKED, VARIANT_MXFP8_SYNC, \
     VARIANT_PACKED_SPLITK = 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11
 DTYPE_BF16, DTYPE_F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 
 class SwiGLUError(RuntimeError):
@@ -134,6 +138,16 @@ def load():
         "swiglu_quantize_mxfp4": ([p, p, p, p, i64, i64, p], st),
         "swiglu_dequantize_mxfp4": ([p, p, p, p, i64, i64, p], st),
         "swiglu_forward_mxfp4": ([p, p, p, p, p, p, i64, i64, i64, i32, p], st),
+        "swiglu_route_scored": ([p, p, p, p, p, p, p, p, i64, i64, i64, i64, ctypes.c_int, i32,
+                                 ctypes.c_float, i32, i32, i32, ctypes.c_int, p], st),
+        "swiglu_int8_packed_bytes": ([i64, i64], i64),
+        "swiglu_pack_int8_fragments": ([p, p, p, i64, i64, i64, p], st),
+        "swiglu_quantize_int8": ([p, p, p, p, i64, i64, p], st),
+        "swiglu_forward_int8": ([p, p, p, p, p, p, i64, i64, i64, i32, p], st),
+        "swiglu_matmul_int8": ([p, p, p, p, p, p, i64, i64, i64, i32, p], st),
+        "swiglu_grouped_forward_int8": ([p, p, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, i32,
+                                         p], st),
+        "swiglu_grouped_matmul_int8": ([p, p, p, p, p, p, p, p, i64, i64, i64, i64, i32, p], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -439,6 +453,65 @@ def swiglu_forward_mxfp4(handle, Q, SQ, W, SW, Y, M, N, K, variant=-1, stream=No
     """Y [M, N] of activations (Q, SQ) [M, K] and paired weights (W, SW) [2N, K] in MXFP4."""
     _check(load().swiglu_forward_mxfp4(handle, _ptr(Q), _ptr(SQ), _ptr(W), _ptr(SW), _ptr(Y), M,
                                        N, K, variant, _stream(stream)), "swiglu_forward_mxfp4")
+
+
+# ---- scored router, 8-bit integers ---------------------------------------------------
+def swiglu_route_scored(handle, logits, bias, weights, experts, offsets, rows, workspace, T, E, k,
+                        score=SCORE_SOFTMAX, renormalize=True, scale=1.0, groups=1, top_groups=1,
+                        group_best=1, dtype=DTYPE_F32, stream=None):
+    """swiglu_route on softmax or sigmoid scores: the k largest score + bias (fp32 [E] or None)
+    among the top_groups best of `groups` groups of experts; weights are scale times the scores."""
+    _check(load().swiglu_route_scored(handle, _ptr(logits), _ptr(bias), _ptr(weights),
+                                      _ptr(experts), _ptr(offsets), _ptr(rows), _ptr(workspace),
+                                      0 if workspace is None else
+                                      workspace.numel() * workspace.element_size(),
+                                      T, E, k, score, 1 if renormalize else 0, scale, groups,
+                                      top_groups, group_best, dtype, _stream(stream)),
+           "swiglu_route_scored")
+
+
+def swiglu_int8_packed_bytes(rows: int, K: int) -> int:
+    return int(load().swiglu_int8_packed_bytes(rows, K))
+
+
+def swiglu_pack_int8_fragments(handle, W8, P, E, rows, K, stream=None):
+    """int8 W8 [E, rows, K] -> fragment-ordered P (E * swiglu_int8_packed_bytes(rows, K) bytes)."""
+    _check(load().swiglu_pack_int8_fragments(handle, _ptr(W8), _ptr(P), E, rows, K,
+                                             _stream(stream)), "swiglu_pack_int8_fragments")
+
+
+def swiglu_quantize_int8(handle, X, Q, S, rows, K, stream=None):
+    """bf16 X [rows, K] -> int8 codes Q [rows, K] and fp32 scales S [rows]."""
+    _check(load().swiglu_quantize_int8(handle, _ptr(X), _ptr(Q), _ptr(S), rows, K,
+                                       _stream(stream)), "swiglu_quantize_int8")
+
+
+def swiglu_forward_int8(handle, Q, SQ, P, SW, Y, M, N, K, variant=-1, stream=None):
+    """Gated products Y [M, N] of activations (Q, SQ) [M, K] and packed weights of 2 N rows, SW [2 N]."""
+    _check(load().swiglu_forward_int8(handle, _ptr(Q), _ptr(SQ), _ptr(P), _ptr(SW), _ptr(Y), M, N,
+                                      K, variant, _stream(stream)), "swiglu_forward_int8")
+
+
+def swiglu_matmul_int8(handle, Q, SQ, P, SW, Y, M, N, K, variant=-1, stream=None):
+    """Products Y [M, N] of activations (Q, SQ) [M, K] and packed weights of N rows, SW [N]."""
+    _check(load().swiglu_matmul_int8(handle, _ptr(Q), _ptr(SQ), _ptr(P), _ptr(SW), _ptr(Y), M, N,
+                                     K, variant, _stream(stream)), "swiglu_matmul_int8")
+
+
+def swiglu_grouped_forward_int8(handle, Q, SQ, rows, offsets, P, SW, Y, T, R, N, K, E, k=1,
+                                variant=-1, stream=None):
+    """swiglu_grouped_forward on activations (Q, SQ) [T, K] and E packed matrices of 2 N rows."""
+    _check(load().swiglu_grouped_forward_int8(handle, _ptr(Q), _ptr(SQ), _ptr(rows), _ptr(offsets),
+                                              _ptr(P), _ptr(SW), _ptr(Y), T, R, N, K, E, k, variant,
+                                              _stream(stream)), "swiglu_grouped_forward_int8")
+
+
+def swiglu_grouped_matmul_int8(handle, Q, SQ, rows, offsets, P, SW, Y, R, N, K, E, variant=-1,
+                               stream=None):
+    """swiglu_grouped_matmul on activations (Q, SQ) [R, K] and E packed matrices of N rows."""
+    _check(load().swiglu_grouped_matmul_int8(handle, _ptr(Q), _ptr(SQ), _ptr(rows), _ptr(offsets),
+                                             _ptr(P), _ptr(SW), _ptr(Y), R, N, K, E, variant,
+                                             _stream(stream)), "swiglu_grouped_matmul_int8")
 
 
 def swiglu_config_count() -> int:

@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libswiglu.so")
 SOURCES = ["swiglu_kernels.hip", "swiglu_route.hip", "swiglu_grouped.hip", "swiglu_norm.hip",
-           "swiglu_fp4.hip", "swiglu_table.cpp", "swiglu_api.cpp", "swiglu_api_ops.cpp"]
+           "swiglu_fp4.hip", "swiglu_int8.hip", "swiglu_table.cpp",
+           "swiglu_api.cpp", "swiglu_api_ops.cpp"]
 ARCH = "gfx950"
 
 

@@ -1,5 +1,5 @@
-// swiglu_api_ops.cpp -- the extern "C" entry points of the mixture-of-experts and
-// MXFP4 operators.  Checks first (swiglu_checks.hpp), then the device of the
+// swiglu_api_ops.cpp -- the extern "C" entry points of the mixture-of-experts,
+// MXFP4 and 8-bit integer operators.  Checks first (swiglu_checks.hpp), then the device of the
 // handle, then the launch; on any error nothing is enqueued.
 #include "swiglu.h"
 
@@ -35,6 +35,21 @@ swiglu_status_t run_grouped(swiglu_handle_t h, bool up, const void* A, const int
                                  variant, stream));
 }
 
+swiglu_status_t run_int8(swiglu_handle_t h, bool gated, bool grouped, const void* A,
+                         const float* SA, const int32_t* rows, const int32_t* offsets,
+                         const void* W, const float* SW, void* Y, int64_t TA, int64_t R, int64_t N,
+                         int64_t K, int64_t E, int64_t k, int32_t variant, hipStream_t stream) {
+  if (!h || variant >= kInt8Variants) return SWIGLU_ERR_INVALID_ARG;
+  const Int8Call call{gated,       grouped, (const uint8_t*)A, SA, rows, offsets, (const uint8_t*)W,
+                      SW,          (uint16_t*)Y, TA, R, N, K, E, k, handle_cu_count(h)};
+  bool noop;
+  const int c = checks::int8_product(call, variant, &noop);
+  if (c != checks::kOk || noop) return (swiglu_status_t)c;
+  const swiglu_status_t st = check_device(h);
+  if (st != SWIGLU_OK) return st;
+  return launched(launch_int8(call, variant, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -58,6 +73,27 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
   if (st != SWIGLU_OK) return st;
   return launched(launch_route(logits, dtype == SWIGLU_DTYPE_F32, weights, experts, offsets, rows,
                                workspace, (int)T, (int)E, (int)k, renormalize != 0, stream));
+}
+
+swiglu_status_t swiglu_route_scored(swiglu_handle_t h, const void* logits, const float* bias,
+                                    float* weights, int32_t* experts, int32_t* offsets,
+                                    int32_t* rows, void* workspace, int64_t workspace_bytes,
+                                    int64_t T, int64_t E, int64_t k, swiglu_score_t score,
+                                    int32_t renormalize, float scale, int32_t groups,
+                                    int32_t top_groups, int32_t group_best, swiglu_dtype_t dtype,
+                                    hipStream_t stream) {
+  if (!h) return SWIGLU_ERR_INVALID_ARG;
+  int c = checks::route(logits, weights, experts, offsets, rows, workspace, workspace_bytes, T, E,
+                        k, (int)dtype);
+  if (c != checks::kOk) return (swiglu_status_t)c;
+  const RouteScore s{bias,   score == SWIGLU_SCORE_SIGMOID, scale, groups, top_groups, group_best};
+  c = checks::route_score(s, weights, experts, offsets, rows, workspace, T, E, k, (int)score);
+  if (c != checks::kOk) return (swiglu_status_t)c;
+  const swiglu_status_t st = check_device(h);
+  if (st != SWIGLU_OK) return st;
+  return launched(launch_route_scored(logits, dtype == SWIGLU_DTYPE_F32, weights, experts, offsets,
+                                      rows, workspace, (int)T, (int)E, (int)k, renormalize != 0, s,
+                                      stream));
 }
 
 swiglu_status_t swiglu_grouped_forward(swiglu_handle_t h, const void* A, const int32_t* rows,
@@ -139,6 +175,61 @@ swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const voi
   const swiglu_status_t st = check_device(h);
   if (st != SWIGLU_OK) return st;
   return launched(launch_forward_mxfp4(call, variant, stream));
+}
+
+int64_t swiglu_int8_packed_bytes(int64_t rows, int64_t K) {
+  if (rows <= 0 || K <= 0 || rows > 0x7fffffffLL || K > 0x7fffffffLL) return 0;
+  return int8_packed_bytes(rows, K);
+}
+
+swiglu_status_t swiglu_pack_int8_fragments(swiglu_handle_t h, const void* W8, void* P, int64_t E,
+                                           int64_t rows, int64_t K, hipStream_t stream) {
+  if (!h) return SWIGLU_ERR_INVALID_ARG;
+  bool noop;
+  const int c = checks::pack_int8(W8, P, E, rows, K, &noop);
+  if (c != checks::kOk || noop) return (swiglu_status_t)c;
+  const swiglu_status_t st = check_device(h);
+  if (st != SWIGLU_OK) return st;
+  return launched(launch_pack_int8((const uint8_t*)W8, (uint8_t*)P, E, (int)rows, (int)K, stream));
+}
+
+swiglu_status_t swiglu_quantize_int8(swiglu_handle_t h, const void* X, void* Q, float* S,
+                                     int64_t rows, int64_t K, hipStream_t stream) {
+  if (!h) return SWIGLU_ERR_INVALID_ARG;
+  bool noop;
+  const int c = checks::quantize_int8(X, Q, S, rows, K, &noop);
+  if (c != checks::kOk || noop) return (swiglu_status_t)c;
+  const swiglu_status_t st = check_device(h);
+  if (st != SWIGLU_OK) return st;
+  return launched(launch_quantize_int8((const uint16_t*)X, (uint8_t*)Q, S, (int)rows, (int)K, stream));
+}
+
+swiglu_status_t swiglu_forward_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                    const void* P, const float* SW, void* Y, int64_t M, int64_t N,
+                                    int64_t K, int32_t variant, hipStream_t stream) {
+  return run_int8(h, true, false, Q, SQ, nullptr, nullptr, P, SW, Y, M, M, N, K, 1, 1, variant, stream);
+}
+
+swiglu_status_t swiglu_matmul_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                   const void* P, const float* SW, void* Y, int64_t M, int64_t N,
+                                   int64_t K, int32_t variant, hipStream_t stream) {
+  return run_int8(h, false, false, Q, SQ, nullptr, nullptr, P, SW, Y, M, M, N, K, 1, 1, variant, stream);
+}
+
+swiglu_status_t swiglu_grouped_forward_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                            const int32_t* rows, const int32_t* offsets,
+                                            const void* P, const float* SW, void* Y, int64_t T,
+                                            int64_t R, int64_t N, int64_t K, int64_t E, int64_t k,
+                                            int32_t variant, hipStream_t stream) {
+  return run_int8(h, true, true, Q, SQ, rows, offsets, P, SW, Y, T, R, N, K, E, k, variant, stream);
+}
+
+swiglu_status_t swiglu_grouped_matmul_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                           const int32_t* rows, const int32_t* offsets,
+                                           const void* P, const float* SW, void* Y, int64_t R,
+                                           int64_t N, int64_t K, int64_t E, int32_t variant,
+                                           hipStream_t stream) {
+  return run_int8(h, false, true, Q, SQ, rows, offsets, P, SW, Y, R, R, N, K, E, 1, variant, stream);
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
-// swiglu_checks.hpp -- argument checks of the mixture-of-experts and MXFP4 entry
-// points: host code only, no device and no handle, so that they can be tried
+// swiglu_checks.hpp -- argument checks of the mixture-of-experts, MXFP4 and 8-bit
+// integer entry points: host code only, no device and no handle, so that they can be tried
 // anywhere.  Each returns a swiglu_status_t value; *noop is set when there is
 // nothing to compute.
 #pragma once
@@ -70,6 +70,22 @@ inline int route(const void* logits, const void* weights, const void* experts, c
   if (clash({{weights, 4 * T * k}, {experts, 4 * T * k}, {offsets, 4 * (E + 1)}, {rows, 4 * T * k},
              {ws, need}},
             {{logits, (long long)size * T * E}}))
+    return kInvalid;
+  return kOk;
+}
+
+// on top of route()
+inline int route_score(const RouteScore& s, const void* weights, const void* experts,
+                       const void* offsets, const void* rows, const void* ws, long long T,
+                       long long E, long long k, int score) {
+  if (score != 0 && score != 1) return kInvalid;
+  if (s.groups < 1 || s.top_groups < 1 || s.top_groups > s.groups || E % s.groups != 0 ||
+      (s.group_best != 1 && s.group_best != 2) || k > s.top_groups * (E / s.groups))
+    return kInvalid;
+  if (s.groups > kMaxGroups || !aligned(s.bias, 4)) return kUnsupported;
+  if (clash({{weights, 4 * T * k}, {experts, 4 * T * k}, {offsets, 4 * (E + 1)}, {rows, 4 * T * k},
+             {ws, route_workspace_bytes(T, E, k)}},
+            {{s.bias, 4 * E}}))
     return kInvalid;
   return kOk;
 }
@@ -180,6 +196,74 @@ inline int forward_mxfp4(const Fp4Call& c, bool* noop) {
   if (clash({{c.Y, 2 * c.M * c.N}},
             {{c.A, (long long)a128}, {c.SA, (long long)a128 / 16}, {c.W, (long long)w128},
              {c.SW, (long long)w128 / 16}}))
+    return kInvalid;
+  return kOk;
+}
+
+// 32-bit sums of products of codes: K 2^14 < 2^31
+constexpr long long kMaxInt8K = (1LL << 17) - 1;
+
+inline int quantize_int8(const void* X, const void* Q, const void* S, long long rows, long long K,
+                         bool* noop) {
+  *noop = false;
+  if (rows < 0 || K < 0) return kInvalid;
+  if (rows == 0 || K == 0) {
+    *noop = true;
+    return kOk;
+  }
+  if (!X || !Q || !S) return kInvalid;
+  if (K % 16 != 0 || K > kMaxInt8K || rows > kMaxInt || int8_quantize_threads(rows, K) > kMaxThreads)
+    return kUnsupported;
+  if (!aligned16({X, Q}) || !aligned(S, 4)) return kUnsupported;
+  if (clash({{Q, rows * K}, {S, 4 * rows}}, {{X, 2 * rows * K}})) return kInvalid;
+  return kOk;
+}
+
+inline int pack_int8(const void* W8, const void* P, long long E, long long rows, long long K,
+                     bool* noop) {
+  *noop = false;
+  if (E < 0 || rows < 0 || K < 0) return kInvalid;
+  if (E == 0 || rows == 0 || K == 0) {
+    *noop = true;
+    return kOk;
+  }
+  if (!W8 || !P) return kInvalid;
+  if (K % 16 != 0 || rows > kMaxInt || K > kMaxInt) return kUnsupported;
+  const long long bytes = int8_packed_bytes(rows, K);
+  if (bytes >= kMax2G || mul(E, bytes) > kMaxTotal || !aligned16({W8, P})) return kUnsupported;
+  if (clash({{P, E * bytes}}, {{W8, E * rows * K}})) return kInvalid;
+  return kOk;
+}
+
+inline int int8_product(const Int8Call& c, int variant, bool* noop) {
+  *noop = false;
+  if (c.TA < 0 || c.R < 0 || c.N < 0 || c.K < 0 || c.E < 1 || c.k < 1) return kInvalid;
+  if (c.R == 0 || c.N == 0) {
+    *noop = true;
+    return kOk;
+  }
+  if (!c.Y || (c.grouped && (!c.rows || !c.offsets)) ||
+      (c.K > 0 && (!c.W || !c.SW || (c.TA > 0 && (!c.A || !c.SA)))))
+    return kInvalid;
+  if (c.E > kMaxExperts || c.TA > kMaxInt || c.R > kMaxInt - 1024 || c.k > kMaxInt ||
+      c.N > (1LL << 23) || c.N % 8 != 0 || c.K % 16 != 0 || c.K > kMaxInt8K)
+    return kUnsupported;
+  if (!aligned16({c.A, c.W, c.SW, c.Y}) || !aligned(c.SA, 4) || !aligned(c.rows, 4) ||
+      !aligned(c.offsets, 4))
+    return kUnsupported;
+  // 32-bit byte offsets inside A and inside one matrix; the experts and the rows
+  // of Y are addressed with 64 bits
+  const long long abytes = mul(c.TA, c.K), wbytes = int8_packed_bytes(c.C(), c.K);
+  const long long ybytes = mul(c.R, 2 * c.N), wall = mul(c.E, wbytes);
+  if (abytes >= kMax2G || wbytes >= kMax2G || wall > kMaxTotal || ybytes > kMaxTotal)
+    return kUnsupported;
+  long long threads, y;
+  int8_launch_size(c, variant, &threads, &y);
+  if (threads > kMaxThreads || y > 65535) return kUnsupported;
+  const long long some = c.K > 0 ? 1 : 0;  // no scales are read where there is nothing to scale
+  if (clash({{c.Y, ybytes}},
+            {{c.A, abytes}, {c.SA, some * 4 * c.TA}, {c.W, wall}, {c.SW, some * 4 * c.E * c.C()},
+             {c.rows, 4 * c.R}, {c.offsets, 4 * (c.E + 1)}}))
     return kInvalid;
   return kOk;
 }

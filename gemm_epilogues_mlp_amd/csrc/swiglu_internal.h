@@ -118,6 +118,17 @@ long long route_workspace_bytes(long long T, long long E, long long k);
 hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* experts,
                         int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
                         bool renorm, hipStream_t stream);
+// The scored form: a score for each logit, a bias that steers the choice, groups of experts.
+struct RouteScore {
+  const float* bias;  // [E] or null
+  int sigmoid;        // else softmax
+  float scale;
+  int groups, top_groups, group_best;
+};
+constexpr int kMaxGroups = 64;
+hipError_t launch_route_scored(const void* logits, bool f32, float* weights, int32_t* experts,
+                               int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
+                               bool renorm, const RouteScore& score, hipStream_t stream);
 // Grouped products; TA: rows of A, variant < 0: by rule
 constexpr int kGroupedVariants = 5;
 long long grouped_threads(bool up, long long R, long long N, long long E, int variant);
@@ -158,6 +169,34 @@ hipError_t launch_quantize_mxfp4(const uint16_t* X, uint8_t* Q, uint8_t* S, int 
                                  hipStream_t stream);
 hipError_t launch_dequantize_mxfp4(const uint8_t* Q, const uint8_t* S, uint16_t* X, int rows,
                                    int K, hipStream_t stream);
+
+// ---- 8-bit integers (swiglu_int8.hip) -----------------------------------------------
+// Bytes of a fragment-ordered matrix of `rows` rows.
+inline long long int8_packed_bytes(long long rows, long long K) {
+  return (rows + 31) / 32 * ((K + 127) / 128) * 4096;
+}
+struct Int8Call {
+  bool gated, grouped;
+  const uint8_t* A;        // [TA, K] codes
+  const float* SA;         // [TA]
+  const int32_t* rows;     // grouped only
+  const int32_t* offsets;
+  const uint8_t* W;        // E packed matrices
+  const float* SW;
+  uint16_t* Y;             // [R, N]
+  long long TA, R, N, K, E, k;
+  int cu_count;
+  long long C() const { return gated ? 2 * N : N; }  // weight rows
+};
+constexpr int kInt8Variants = 5;
+void int8_launch_size(const Int8Call& c, int variant, long long* threads, long long* y);
+hipError_t launch_int8(const Int8Call& c, int variant, hipStream_t stream);
+// threads of the quantising launch
+long long int8_quantize_threads(long long rows, long long K);
+hipError_t launch_quantize_int8(const uint16_t* X, uint8_t* Q, float* S, int rows, int K,
+                                hipStream_t stream);
+hipError_t launch_pack_int8(const uint8_t* W8, uint8_t* P, long long E, int rows, int K,
+                            hipStream_t stream);
 
 // Per-shape choice (tile table + fallback rule).  variant is SYNC, INTERLEAVE
 // or GEMM; returns a config id of that variant.

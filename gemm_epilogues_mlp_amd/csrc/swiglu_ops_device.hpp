@@ -227,6 +227,15 @@ __device__ __forceinline__ float e8m0_scale(int e) {
   return __builtin_bit_cast(float, e > 0 ? (uint32_t)e << 23 : 1u << 22);
 }
 
+// ---- 8-bit integers ---------------------------------------------------------------
+// v_mfma_i32_32x32x32_i8: lane l holds row or column l % 32 and the 16 consecutive k
+// of half l / 32 in 16 bytes; the output layout is that of the bf16 32x32x16.
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ i32x16 mfma32_i8(const u32x4& a, const u32x4& b, const i32x16& c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
+                                               __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
 // ---- launches ---------------------------------------------------------------------
 // Judged by hipLaunchKernel's own return value, as every launch of the library.
 template <typename... P, typename... Args>

@@ -179,17 +179,153 @@ __device__ __forceinline__ void route_token_keys(const RouteArgs& a, int t, bool
   weight = mine ? p / total : 0.0f;
 }
 
+// ---- scored choice -------------------------------------------------------------------
+// swiglu_route_scored: with a score s of each logit (its sigmoid, or the softmax over the
+// open ones) and c = s + bias, the k largest c of the kept groups are chosen, and s is
+// the weight.  Scores, sums and comparisons are in 64 bits: neighbours among some hundred
+// scores between 0 and 1 come as close as fp32 rounds exp, and the choice is to be that
+// of the definition.
+struct NoScore {};
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t x = __builtin_bit_cast(uint64_t, v);
+  const int lo = (int)(uint32_t)x, hi = (int)(uint32_t)(x >> 32);
+  const uint32_t a = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xf, 0xf, false);
+  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)b << 32 | a);
+}
+// over aligned groups of G lanes (16, 32 or 64); every lane receives the same bits
+template <int G, typename F>
+__device__ __forceinline__ double group_fold(double v, F f) {
+  v = f(v, dpp_d<kDppXor1>(v));
+  v = f(v, dpp_d<kDppXor2>(v));
+  v = f(v, dpp_d<kDppHalfMirror>(v));
+  v = f(v, dpp_d<kDppMirror>(v));
+  if (G >= 32) v = f(v, __shfl_xor(v, 16));
+  if (G >= 64) v = f(v, __shfl_xor(v, 32));
+  return v;
+}
+constexpr double kNegInfD = -__builtin_inf();
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+
+// LDS of one token.
+template <int N>
+struct ScoreRoom {
+  double c[N];             // of all experts
+  double value[kMaxGroups];
+  double picked[64];       // scores of the chosen ones
+  int index[64];
+};
+
+// As route_token.
+template <typename In, int G, int C>
+__device__ __forceinline__ void route_token_scored(const RouteArgs& a, const RouteScore& sc, int t,
+                                                   bool in, ScoreRoom<G * C>& room,
+                                                   int32_t& expert, float& weight) {
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  float x[C];
+  load_logits<C>((const In*)a.logits + (size_t)(in ? t : 0) * a.E, in ? a.E : 0, gl * C, a.vec, x);
+  double s[C], c[C];
+  if (sc.sigmoid) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) s[j] = 1.0 / (1.0 + exp(-(double)x[j]));
+  } else {
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < C; ++j) m = fmaxf(m, x[j]);
+    m = group_max<G>(m);
+    m = m > kNegInf ? m : 0.0f;
+    double total = 0.0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      s[j] = x[j] == m ? 1.0 : exp((double)x[j] - (double)m);
+      total += s[j];
+    }
+    total = group_fold<G>(total, [](double u, double v) { return u + v; });
+#pragma unroll
+    for (int j = 0; j < C; ++j) s[j] = total > 0.0 ? s[j] / total : 0.0;
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int e = gl * C + j;
+    const double v = s[j] + (sc.bias && e < a.E ? (double)sc.bias[e] : 0.0);
+    c[j] = x[j] > kNegInf && v == v ? v : kNegInfD;
+  }
+  if (sc.groups > 1) {
+    const int size = a.E / sc.groups;
+#pragma unroll
+    for (int j = 0; j < C; ++j) room.c[gl * C + j] = c[j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (int g = gl; g < sc.groups; g += G) {
+      double first = kNegInfD, second = kNegInfD;
+      for (int i = 0; i < size; ++i) {
+        const double v = room.c[g * size + i];
+        second = larger(second, v < first ? v : first);
+        first = larger(first, v);
+      }
+      room.value[g] = sc.group_best == 2 && second > kNegInfD ? first + second : first;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int e = gl * C + j;
+      if (e >= a.E) continue;
+      const int mine = e / size;
+      const double value = room.value[mine];
+      int before = 0;
+      for (int g = 0; g < sc.groups; ++g) {
+        const double v = room.value[g];
+        before += v > value || (v == value && g < mine);
+      }
+      if (before >= sc.top_groups) c[j] = kNegInfD;
+    }
+  }
+  bool open = false;
+  for (int i = 0; i < a.k; ++i) {
+    double v = c[0], p = s[0];
+    int bj = 0;
+#pragma unroll
+    for (int j = 1; j < C; ++j)
+      if (c[j] > v) v = c[j], p = s[j], bj = j;
+    const double best = group_fold<G>(v, larger);
+    if (gl == i) open = best > kNegInfD;
+    const unsigned long long group = (G == 64 ? ~0ull : ((1ull << (G & 63)) - 1)) << (lane & ~(G - 1));
+    if (lane == __ffsll(__ballot(v == best) & group) - 1) {
+      room.index[i] = gl * C + bj;
+      room.picked[i] = p;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j == bj) c[j] = kNegInfD;
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  open = open && gl < a.k;
+  double p = open ? room.picked[gl] : 0.0;
+  expert = open ? room.index[gl] : -1;
+  if (a.renorm) {
+    const double total = group_fold<G>(p, [](double u, double v) { return u + v; });
+    p = total > 0.0 ? p / total : 0.0;
+  }
+  weight = open ? (float)(p * (double)sc.scale) : 0.0f;
+}
+
 // Tokens [t0, t1) by the workgroup: results to memory, slots counted in hist,
 // and with `slots` the choices kept in LDS too.
-template <typename In, int G, int C>
-__device__ __forceinline__ void route_tokens(const RouteArgs& a, int t0, int t1, int* picked,
-                                             int* hist, int* slots) {
+template <typename In, int G, int C, typename Score>
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, const Score& score, int t0, int t1,
+                                             int* picked, ScoreRoom<G * C>* rooms, int* hist,
+                                             int* slots) {
   const int per = blockDim.x / G, gl = threadIdx.x & (G - 1), first = (int)threadIdx.x / G;
   for (int t = t0 + first; t - first < t1; t += per) {
     const bool in = t < t1;
     int32_t e;
     float w;
-    if constexpr (std::is_same_v<In, uint16_t>)
+    if constexpr (!std::is_same_v<Score, NoScore>)
+      route_token_scored<In, G, C>(a, score, t, in, rooms[first], e, w);
+    else if constexpr (std::is_same_v<In, uint16_t>)
       route_token_keys<G, C>(a, t, in, e, w);
     else
       route_token<In, G, C>(a, t, in, picked + (threadIdx.x & ~(G - 1)), e, w);
@@ -304,8 +440,10 @@ constexpr long long kRouteSmall = 512;
 
 // ---- one workgroup does everything -------------------------------------------------
 constexpr int kSmallThreads = 512;
-template <typename In, int G, int C>
-__global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a) {
+template <typename In, int G, int C, typename Score>
+__global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a, Score score) {
+  constexpr bool kScored = !std::is_same_v<Score, NoScore>;
+  __shared__ __attribute__((aligned(16))) ScoreRoom<G * C> rooms[kScored ? kSmallThreads / G : 1];
   __shared__ __attribute__((aligned(16))) int next[kSmallThreads / 64 * G * C];
   __shared__ __attribute__((aligned(16))) int hist[G * C];
   __shared__ __attribute__((aligned(16))) int offset[G * C + 1];
@@ -315,7 +453,7 @@ __global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a)
   for (int i = threadIdx.x; i < nw * a.E; i += blockDim.x) next[i] = 0;
   for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
-  route_tokens<In, G, C>(a, 0, a.T, picked, hist, slots);
+  route_tokens<In, G, C>(a, score, 0, a.T, picked, rooms, hist, slots);
   __syncthreads();
   const RouteShare share = route_share(slots, 0, n);
   route_count(a, slots, share, next);
@@ -335,14 +473,17 @@ __global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a)
 // tokens, 3.0 at 200 and 2000.)
 constexpr int kSelectThreads = 512, kPlaceThreads = 1024;
 constexpr int kMaxRouteBlocks = 256;  // one on every CU
-template <typename In, int G, int C>
-__global__ __launch_bounds__(kSelectThreads) void route_select_kernel(RouteArgs a, int stride) {
+template <typename In, int G, int C, typename Score>
+__global__ __launch_bounds__(kSelectThreads) void route_select_kernel(RouteArgs a, Score score,
+                                                                      int stride) {
+  constexpr bool kScored = !std::is_same_v<Score, NoScore>;
+  __shared__ __attribute__((aligned(16))) ScoreRoom<G * C> rooms[kScored ? kSelectThreads / G : 1];
   __shared__ __attribute__((aligned(16))) int hist[G * C];
   __shared__ __attribute__((aligned(16))) int picked[kSelectThreads];
   for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
   const int t0 = blockIdx.x * a.tokens;
-  route_tokens<In, G, C>(a, t0, min(t0 + a.tokens, a.T), picked, hist, nullptr);
+  route_tokens<In, G, C>(a, score, t0, min(t0 + a.tokens, a.T), picked, rooms, hist, nullptr);
   __syncthreads();
   for (int i = threadIdx.x; i < a.E; i += blockDim.x)
     a.counts[(size_t)blockIdx.x * stride + i] = hist[i];
@@ -432,37 +573,50 @@ long long route_workspace_bytes(long long T, long long E, long long k) {
   return route_blocks(T, E, k, &tokens) * ((E + 3) / 4 * 4) * 4;
 }
 
-template <typename In, int G, int C>
-static hipError_t launch_route_as(RouteArgs a, hipStream_t stream) {
+template <typename In, int G, int C, typename Score>
+static hipError_t launch_route_as(RouteArgs a, const Score& score, hipStream_t stream) {
   if ((long long)a.T * a.k <= kRouteSmall) {
     // as many waves as the tokens fill: a token alone takes 4.2 us, with all 8 waves 4.8
     const int threads = std::max(64, std::min((a.T * G + 63) / 64 * 64, kSmallThreads));
-    return launch_op(route_small_kernel<In, G, C>, dim3(1), dim3(threads), stream, a);
+    return launch_op(route_small_kernel<In, G, C, Score>, dim3(1), dim3(threads), stream, a, score);
   }
   long long tokens;
   const int blocks = route_blocks(a.T, a.E, a.k, &tokens), stride = (a.E + 3) / 4 * 4;
   a.tokens = (int)tokens;
-  const hipError_t e = launch_op(route_select_kernel<In, G, C>, dim3(blocks), dim3(kSelectThreads),
-                                 stream, a, stride);
+  const hipError_t e = launch_op(route_select_kernel<In, G, C, Score>, dim3(blocks),
+                                 dim3(kSelectThreads), stream, a, score, stride);
   if (e != hipSuccess) return e;
   return launch_op(route_place_kernel<G * C>, dim3(blocks), dim3(kPlaceThreads), stream, a, stride);
 }
-template <typename In>
-static hipError_t launch_route_in(const RouteArgs& a, hipStream_t stream) {
+template <typename In, typename Score>
+static hipError_t launch_route_in(const RouteArgs& a, const Score& score, hipStream_t stream) {
   const int lanes = route_lanes(a.E, a.k);
-  if (lanes == 16) return launch_route_as<In, 16, 8>(a, stream);
-  if (lanes == 32) return launch_route_as<In, 32, 8>(a, stream);
-  if (a.E <= 512) return launch_route_as<In, 64, 8>(a, stream);
-  return launch_route_as<In, 64, 16>(a, stream);
+  if (lanes == 16) return launch_route_as<In, 16, 8>(a, score, stream);
+  if (lanes == 32) return launch_route_as<In, 32, 8>(a, score, stream);
+  if (a.E <= 512) return launch_route_as<In, 64, 8>(a, score, stream);
+  return launch_route_as<In, 64, 16>(a, score, stream);
+}
+template <typename Score>
+static hipError_t launch_route_with(const void* logits, bool f32, float* weights, int32_t* experts,
+                                    int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
+                                    bool renorm, const Score& score, hipStream_t stream) {
+  const int row = E * (f32 ? 4 : 2);
+  const int vec = ((uintptr_t)logits % 16 == 0 && row % 16 == 0) ? 1 : 0;
+  const RouteArgs a{logits, weights, experts, offsets, rows, (int32_t*)ws, T, E, k, renorm, vec, 0};
+  return f32 ? launch_route_in<float>(a, score, stream) : launch_route_in<uint16_t>(a, score, stream);
 }
 
 hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* experts,
                         int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
                         bool renorm, hipStream_t stream) {
-  const int row = E * (f32 ? 4 : 2);
-  const int vec = ((uintptr_t)logits % 16 == 0 && row % 16 == 0) ? 1 : 0;
-  const RouteArgs a{logits, weights, experts, offsets, rows, (int32_t*)ws, T, E, k, renorm, vec, 0};
-  return f32 ? launch_route_in<float>(a, stream) : launch_route_in<uint16_t>(a, stream);
+  return launch_route_with(logits, f32, weights, experts, offsets, rows, ws, T, E, k, renorm,
+                           NoScore{}, stream);
+}
+hipError_t launch_route_scored(const void* logits, bool f32, float* weights, int32_t* experts,
+                               int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
+                               bool renorm, const RouteScore& score, hipStream_t stream) {
+  return launch_route_with(logits, f32, weights, experts, offsets, rows, ws, T, E, k, renorm, score,
+                           stream);
 }
 
 }  // namespace swiglu

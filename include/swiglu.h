@@ -504,6 +504,38 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
                              int64_t workspace_bytes, int64_t T, int64_t E, int64_t k,
                              int32_t renormalize, swiglu_dtype_t dtype, hipStream_t stream);
 
+/* How swiglu_route_scored turns a logit x into a score. */
+typedef enum {
+  SWIGLU_SCORE_SOFTMAX = 0, /* exp(x) over the sum of it over the token's open logits */
+  SWIGLU_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-x))                                      */
+} swiglu_score_t;
+
+/* swiglu_route with a score for each expert, a bias that only steers the choice
+ * and a choice limited to groups of experts.  For each of T tokens:
+ *   s_e = score of logit e;  c_e = s_e + bias[e]      bias fp32 [E] or NULL (0)
+ *   the experts are `groups` groups of E / groups consecutive ones; a group's value is the sum
+ *   of its group_best (1 or 2) largest c, or of what open ones it has; the top_groups groups of
+ *   the largest value are kept, the lower index first among equals
+ *   the k largest c of the kept groups are chosen, the lower index first among equals
+ *   weights [T, k]  fp32, scale s_i, divided by the sum of s over the chosen experts with
+ *                   renormalize != 0 (0 where that sum is 0)
+ * Scores, sums and comparisons are in 64 bits, so that what decides between two
+ * experts is not how exp rounds.  A logit of -inf or NaN is masked off, and so is an
+ * expert whose c is -inf or NaN; a group without open experts is not kept.  In a
+ * softmax an infinite largest logit shares the weight with its equals.  experts,
+ * rows, offsets, the places left over, the workspace (swiglu_route_workspace_bytes),
+ * the limits and the errors are swiglu_route's.  Also INVALID_ARG: E not a
+ * multiple of groups, top_groups outside [1, groups], k > top_groups (E / groups),
+ * group_best other than 1 or 2, an unknown score, a bias that an output overlaps;
+ * UNSUPPORTED: groups > 64, a bias not aligned to 4 bytes. */
+swiglu_status_t swiglu_route_scored(swiglu_handle_t h, const void* logits, const float* bias,
+                                    float* weights, int32_t* experts, int32_t* offsets,
+                                    int32_t* rows, void* workspace, int64_t workspace_bytes,
+                                    int64_t T, int64_t E, int64_t k, swiglu_score_t score,
+                                    int32_t renormalize, float scale, int32_t groups,
+                                    int32_t top_groups, int32_t group_best, swiglu_dtype_t dtype,
+                                    hipStream_t stream);
+
 /* Y[i] = SiLU(a G_e) * (a U_e) for the sorted rows i in [offsets[e],
  * offsets[e + 1]), with a = A[rows[i] / k], A [T, K], W [E, K, 2N] holding G_e
  * in the even and U_e in the odd columns of expert e (the W_fused order), Y
@@ -592,6 +624,80 @@ swiglu_status_t swiglu_dequantize_mxfp4(swiglu_handle_t h, const void* Q, const 
 swiglu_status_t swiglu_forward_mxfp4(swiglu_handle_t h, const void* Q, const void* SQ,
                                      const void* W, const void* SW, void* Y, int64_t M, int64_t N,
                                      int64_t K, int32_t variant, hipStream_t stream);
+
+/* ---- 8-bit integers ------------------------------------------------------------
+ * Symmetric codes from -128 to 127 with one fp32 scale for each row: a token's for
+ * activations, an output channel's for weights.  A code q of row r stands for
+ * S[r] q, so with exact integer sums
+ *   p[m, c] = (SQ[m] * sum_k Q[m, k] W[c, k]) * SW[c]
+ * where the sum is converted to fp32 first.  Activations Q [rows, K] are row-major;
+ * weights, given as rows W8 [C, K] (gated: C = 2 N, row 2n Gate column n, row 2n + 1 Up
+ * column n, see swiglu_pack_kmajor; plain: C = N, row n output column n), are
+ * stored once in the order the 32x32x32 matrix instructions read them, E
+ * matrices one after another.  With B = ceil(C / 32) and G = ceil(K / 128):
+ *   P[((((e B + b) G + g) 4 + s) 2 + h) 512 + 16 i + j] = W8[e][32 b + i][128 g + 32 s + 16 h + j]
+ * for s < 4, h < 2, i < 32, j < 16, and 0 for rows and k past the matrix
+ * (swiglu_pack_int8_fragments writes them, and the products rely on it).  A scale of NaN
+ * makes its row's products NaN.  A smoothing of activations by channel folds into the norm
+ * before them, or into SW of the Up rows before the down products. */
+
+/* Bytes of P for one matrix of C = `rows` rows: ceil(rows / 32) * ceil(K / 128) * 4096
+ * (0 when a size is <= 0 or out of range). */
+int64_t swiglu_int8_packed_bytes(int64_t rows, int64_t K);
+
+/* P (E * swiglu_int8_packed_bytes(rows, K) bytes, padding included) from int8 W8
+ * [E, rows, K].  A byte copy done once per weight set.  K % 16 == 0, 16-byte aligned
+ * tensors, each matrix under 2 GiB packed (else UNSUPPORTED); P must not overlap W8
+ * (INVALID_ARG).  A size of 0 is a no-op. */
+swiglu_status_t swiglu_pack_int8_fragments(swiglu_handle_t h, const void* W8, void* P, int64_t E,
+                                           int64_t rows, int64_t K, hipStream_t stream);
+
+/* Codes Q [rows, K] and scales S fp32 [rows] of bf16 X [rows, K]: with a row's largest
+ * magnitude a, S = a / 127 and Q = 127 x / a to the nearest integer, the even one at
+ * a tie (the quotient itself is rounded, not a product with a rounded reciprocal).  A
+ * row of zeros has S = 0 and codes 0; a row with a NaN or an infinity has S = NaN and
+ * codes 0.  Activations on the way, or weights once (rows of W8).  K % 16 == 0,
+ * K < 2^17, 16-byte aligned X and Q, a launch of fewer than 2^32 threads (rows < 2^22
+ * do; else UNSUPPORTED); outputs must not overlap X or each other. */
+swiglu_status_t swiglu_quantize_int8(swiglu_handle_t h, const void* X, void* Q, float* S,
+                                     int64_t rows, int64_t K, hipStream_t stream);
+
+/* Y = bf16(SiLU(g) * u), g and u the Gate and Up products of activations (Q, SQ) [M, K]
+ * with the packed weights P of C = 2 N rows and their scales SW [2 N]; sums in 32-bit
+ * integers.  K = 0 writes Y = 0 and reads no scales.  N % 8 == 0, N <= 2^23,
+ * K % 16 == 0, K < 2^17 (where no sum leaves 32 bits), 16-byte aligned Q, P, SW and Y,
+ * SQ aligned to 4 bytes, Q and P under 2 GiB (else UNSUPPORTED); Y [M, N] may be larger
+ * and must not overlap an input.  variant < 0: chosen from the sizes; 0 ... 4 force one
+ * (tests and tuning), a larger one is INVALID_ARG. */
+swiglu_status_t swiglu_forward_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                    const void* P, const float* SW, void* Y, int64_t M, int64_t N,
+                                    int64_t K, int32_t variant, hipStream_t stream);
+
+/* Y = bf16(p), the plain product with packed weights of C = N rows, SW [N] (the down
+ * product behind swiglu_forward_int8, or any other).  Limits as swiglu_forward_int8. */
+swiglu_status_t swiglu_matmul_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                   const void* P, const float* SW, void* Y, int64_t M, int64_t N,
+                                   int64_t K, int32_t variant, hipStream_t stream);
+
+/* swiglu_grouped_forward on 8-bit integers: Y[i] = SiLU(g) * u for the sorted rows i of each
+ * expert e, g and u the products of activation row rows[i] / k of (Q, SQ) [T, K] with expert
+ * e's matrix of P (E matrices of 2 N rows) and SW [E, 2 N].  Spans, offsets, slots and rows
+ * in no span as there; limits as swiglu_forward_int8 for Q and for one expert's
+ * matrix, E <= 1024, a launch of fewer than 2^32 threads (else UNSUPPORTED). */
+swiglu_status_t swiglu_grouped_forward_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                            const int32_t* rows, const int32_t* offsets,
+                                            const void* P, const float* SW, void* Y, int64_t T,
+                                            int64_t R, int64_t N, int64_t K, int64_t E, int64_t k,
+                                            int32_t variant, hipStream_t stream);
+
+/* swiglu_grouped_matmul on 8-bit integers: Y[rows[i]] = p of row i of (Q, SQ) [R, K] in sorted
+ * order, P of E matrices of N rows, SW [E, N].  A slot outside [0, R) is not written;
+ * a slot must not appear twice.  Limits as swiglu_grouped_forward_int8. */
+swiglu_status_t swiglu_grouped_matmul_int8(swiglu_handle_t h, const void* Q, const float* SQ,
+                                           const int32_t* rows, const int32_t* offsets,
+                                           const void* P, const float* SW, void* Y, int64_t R,
+                                           int64_t N, int64_t K, int64_t E, int32_t variant,
+                                           hipStream_t stream);
 
 /* Number of compiled kernel configurations and their descriptions. */
 int32_t swiglu_config_count(void);

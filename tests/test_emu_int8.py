@@ -1,0 +1,54 @@
+"""CPU bounds and LDS-ordering emulation of the 8-bit integer kernels (no GPU), as
+test_emu_ops.py does for the other operators: every LDS offset, DMA source and global access of
+every variant is checked against the buffers, every LDS access against the barriers and DMA waits,
+and every output element that has to be written is, and no other."""
+import concurrent.futures as cf
+import os
+import subprocess
+import sys
+
+import pytest
+
+COUNTS = ["40,1,0,300,17", "0,0", "1,1,1", "16,64,0,33", "384,129"]
+DENSE = [("dense", gated, v, m, n, k) for gated in (1, 0) for v in range(5)
+         for m, n, k in ((1, 8, 16), (70, 72, 80), (300, 136, 544), (33, 264, 0))]
+GROUPED = [("grouped", gated, v, n, k, 3, 5, c) for gated in (1, 0) for v in range(5)
+           for n, k in ((72, 80), (264, 208), (8, 0)) for c in COUNTS]
+OTHER = [("quantize", rows, k) for rows, k in ((5, 16), (6, 1024), (3, 1040), (2, 9008), (2, 20000), (2, 40000))] + \
+    [("pack", *a) for a in ((1, 1, 16), (3, 40, 144), (2, 64, 256))]
+
+
+@pytest.fixture(scope="module")
+def runs(tmp_path_factory):
+    sys.path.insert(0, os.path.join(os.path.dirname(__file__), "emu"))
+    import build as emu_build
+    import build_int8
+    if emu_build.clangxx() is None:
+        pytest.skip("no host clang++")
+    exe = build_int8.build(str(tmp_path_factory.mktemp("emu_int8")))
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0")
+
+    def run(args):
+        r = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=300, env=env)
+        return r.returncode, r.stdout + r.stderr
+    with cf.ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
+        jobs = DENSE + GROUPED + OTHER
+        yield dict(zip(jobs, ex.map(run, jobs)))
+
+
+def clean(runs, jobs):
+    for job in jobs:
+        rc, out = runs[job]
+        assert rc == 0 and "errors: 0" in out, f"{job}: {out[-3000:]}"
+
+
+def test_dense_launches(runs):
+    clean(runs, DENSE)
+
+
+def test_grouped_launches(runs):
+    clean(runs, GROUPED)
+
+
+def test_quantisation_and_packing(runs):
+    clean(runs, OTHER)
