@@ -179,6 +179,368 @@ __global__ __launch_bounds__(256) void pack_int8_kernel(const uint8_t* __restric
 }
 
 // ============================================================================
+// Many rows: LDS-tiled
+// ============================================================================
+// A tile is BM rows of A against BNW weight rows, as D = W A^T on
+// v_mfma_i32_32x32x32_i8.  K runs in the stored groups of 128 as two stages of 64
+// k each, in a ring of two groups in LDS: 2 KB of every block of 32 weight rows, copied
+// as they are (a fragment is one 16-byte read a lane at 16 x lane), and 64-byte
+// pieces of the rows of A, whose 16-byte chunks are swizzled so that the lanes read
+// together spread over the banks.
+//
+// One workgroup stays on a CU and walks over tiles, the ring running on from one
+// to the next: a tile's last two groups already load the next one's first, and the
+// output goes to memory straight from registers, so that LDS stays the ring's.  What the
+// next tile needs beside that arrives by the same direct loads: its scales and, by
+// expert, the slots of its rows, early in this tile, from which come the row
+// addresses of its loads.  None of these loads is waited for by itself: the ring's own waits
+// let the newest 2 LOADS of a wave be in flight, and more loads in between only make them
+// reach further.
+template <int BM, int BNW, int WGM, int WGN>
+struct Int8Tile {
+  static constexpr int kWaves = WGM * WGN, kThreads = 64 * kWaves;
+  static constexpr int NA = BM / 32, NW = BNW / 32;  // blocks of 32 of the tile
+  static constexpr int FA = NA / WGM, FW = NW / WGN;  // and of a wave
+  static_assert(FA >= 1 && FW >= 1 && FA * WGM == NA && FW * WGN == NW, "wave tile");
+  static constexpr int A_BYTES = NA * 2048, STAGE = (NA + NW) * 2048, GROUP = 2 * STAGE;
+  static constexpr int A_LOADS = 2 * NA / kWaves, W_LOADS = 2 * NW / kWaves;  // 1 KB loads of a wave
+  static constexpr int LOADS = A_LOADS + W_LOADS;
+  static_assert(2 * NA % kWaves == 0 && 2 * NW % kWaves == 0, "every wave loads as much");
+  static_assert(2 * LOADS <= 63, "vmcnt range");
+  // behind the ring, by parity of the tile: scales of its rows of A and of W, slots of its rows
+  static constexpr int SA_OFF = 2 * GROUP, SW_OFF = SA_OFF + 8 * BM, ROW_OFF = SW_OFF + 8 * BNW;
+  static constexpr int TABLE_OFF = ROW_OFF + 8 * BM;  // by expert
+  static constexpr int lds_bytes(bool grouped) {
+    return grouped ? TABLE_OFF + 12 * (int)kMaxExperts : ROW_OFF;
+  }
+  static_assert(lds_bytes(true) <= 160 * 1024, "LDS");
+  static constexpr int kPerCu = lds_bytes(true) <= 80 * 1024 ? 2 : 1;
+  // 64-byte rows: chunk c of row r is stored at c ^ swz(r)
+  __host__ __device__ static constexpr int swz(int row) {
+    return (((row >> 2) & 1) << 1) | (((row >> 1) ^ (row >> 3)) & 1);
+  }
+  // groups run for a tile: what the next one needs is asked for in the first and used two
+  // groups before the end; by expert the slots come before the loads that they address
+  static constexpr int kMinGroups = 2, kMinGroupsGrouped = 4;
+};
+
+template <int OP, bool GROUPED, int BM, int BNW, int WGM, int WGN, int PARTS>
+__global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, int ntn, int group_m) {
+  using C = Int8Tile<BM, BNW, WGM, WGN>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::lds_bytes(GROUPED)];
+  const int lane = threadIdx.x & 63;
+  const int wave_u = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave_u / WGN, wn = wave_u % WGN;
+  const int K = a.K, G = (K + 127) / 128;
+  const int Gp = max(G, GROUPED ? C::kMinGroupsGrouped : C::kMinGroups);
+  const int nblk = (a.C + 31) / 32;
+  const uint32_t wbytes = (uint32_t)nblk * (uint32_t)G * 4096u;  // of one matrix
+
+  // workgroup b runs on XCD b % 8; each XCD owns a contiguous range of tiles, which
+  // its workgroups take in turn
+  const int x = blockIdx.x % 8, nwg = gridDim.x;
+  const int stride = nwg / 8 + (x < nwg % 8 ? 1 : 0);
+  const GroupTable table{reinterpret_cast<int*>(smem + C::TABLE_OFF),
+                         reinterpret_cast<int*>(smem + C::TABLE_OFF) + kMaxExperts,
+                         reinterpret_cast<int*>(smem + C::TABLE_OFF) + 2 * kMaxExperts};
+  int first, end;
+  const int ntm = (a.R + BM - 1) / BM;
+  if constexpr (GROUPED) {
+    group_table<BM>(a.offsets, a.E, a.R, table);
+    const GroupRange range = group_range<BM, PARTS>(a.offsets, a.E, a.R, ntn, x);
+    first = range.begin;
+    end = range.end;
+    __syncthreads();
+  } else {
+    const int ntiles = ntm * ntn;
+    first = x * (ntiles / 8) + min(x, ntiles % 8);
+    end = first + ntiles / 8 + (x < ntiles % 8 ? 1 : 0);
+  }
+  first += (int)blockIdx.x / 8;
+  if (first >= end) return;
+
+  const i32x4 rsA = make_rsrc(a.A, (uint32_t)a.TA * (uint32_t)K);
+  const i32x4 rsSA = make_rsrc(a.SA, K > 0 ? (uint32_t)a.TA * 4u : 0u);
+  const uint32_t lds0 = lds_addr(smem);
+
+  // A tile: rows [pos0, pos0 + rows) against weight rows from tn BNW on; none past the
+  // last one.
+  struct Tile {
+    int expert, pos0, rows, tn;
+  };
+  auto uniform = [](int v) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(v); };
+  auto locate = [&](int t, int from) __attribute__((always_inline)) {
+    Tile o{from, 0, 0, 0};
+    if (t < end) {
+      int local = t, row0 = 0, n = a.R, high_all = ntm;
+      int band_rows = group_m;
+      if constexpr (GROUPED) {
+        o.expert = uniform(group_find(table, a.E, t / ntn, from));
+        row0 = uniform(table.lo[o.expert]);
+        n = uniform(table.n[o.expert]);
+        high_all = (n + BM - 1) / BM;
+        local = t - uniform(table.upto[o.expert] - high_all) * ntn;
+      }
+      // bands of tile rows, column after column
+      const int band = local / (band_rows * ntn), in = local % (band_rows * ntn);
+      const int high = min(high_all - band * band_rows, band_rows);
+      const int tm = band * band_rows + in % high;
+      o.tn = uniform(in / high);
+      o.pos0 = uniform(row0 + tm * BM);
+      o.rows = uniform(min(n - tm * BM, BM));
+    }
+    return o;
+  };
+
+  // ---- loads --------------------------------------------------------------------------
+  // Load q of a wave is 1 KB of a stage, A's before W's: 16 rows of A, or half a stage of one
+  // block of 32 weight rows.  What lies past a tensor comes as zeros; k past K is
+  // zero in W, whatever A has there.
+  const int a_row = lane >> 2;  // of the load's 16
+  uint32_t off[C::LOADS], a_next[C::A_LOADS];
+  auto a_chunk = [&](int row) __attribute__((always_inline)) {
+    return (uint32_t)(((lane & 3) ^ C::swz(row)) * 16);
+  };
+  // offset of the lane's row of A in load q, by the tile's slots
+  auto a_offset = [&](const Tile& o, int par, int q) __attribute__((always_inline)) {
+    const int r = (q * C::kWaves + wave_u) * 16 + a_row;
+    int row = r < o.rows ? o.pos0 + r : -1;
+    if constexpr (GROUPED && OP == I8_GATED) {
+      const int slot = reinterpret_cast<const int*>(smem + C::ROW_OFF + par * 4 * BM)[r];
+      row = r < o.rows && slot >= 0 && slot / a.k < a.TA ? slot / a.k : -1;
+    }
+    return row >= 0 ? (uint32_t)row * (uint32_t)K + a_chunk(r) : kOutOfRange;
+  };
+#pragma unroll
+  for (int q = C::A_LOADS; q < C::LOADS; ++q) {
+    const int c = (q - C::A_LOADS) * C::kWaves + wave_u;
+    off[q] = (uint32_t)(c >> 1) * (uint32_t)G * 4096u + (uint32_t)(c & 1) * 1024u + (uint32_t)lane * 16u;
+  }
+  auto weights = [&](const Tile& o) __attribute__((always_inline)) {
+    return make_rsrc(a.W + (size_t)o.expert * wbytes, wbytes);
+  };
+  // load q of stage HALF of group g of a tile into ring slot `slot`
+  auto dma = [&](const Tile& o, const i32x4& rsW, const uint32_t* rows, int g, int slot, int half,
+                 int q) __attribute__((always_inline)) {
+    const bool in = g < G && o.rows > 0;
+    const uint32_t base = lds0 + slot * C::GROUP + half * C::STAGE;
+    if (q < C::A_LOADS) {
+      lds_dma16(base + (q * C::kWaves + wave_u) * 1024,
+                in ? rows[q] + (uint32_t)(g * 128 + half * 64) : kOutOfRange, rsA);
+    } else {
+      const uint32_t at = (uint32_t)(o.tn * C::NW) * (uint32_t)G * 4096u + (uint32_t)g * 4096u +
+                          (uint32_t)half * 2048u;
+      lds_dma16(base + C::A_BYTES + ((q - C::A_LOADS) * C::kWaves + wave_u) * 1024,
+                off[q] + (in ? at : kOutOfRange), rsW);
+    }
+  };
+  // the slots of a tile's rows, 64 a load
+  auto load_slots = [&](const Tile& o, int par) __attribute__((always_inline)) {
+    if constexpr (GROUPED) {
+      const i32x4 rs = make_rsrc(a.rows + o.pos0, (uint32_t)o.rows * 4u);
+#pragma unroll
+      for (int c0 = 0; c0 < BM / 64; c0 += C::kWaves) {
+        const int c = c0 + wave_u;
+        if (c < BM / 64) lds_dma4(lds0 + C::ROW_OFF + par * 4 * BM + c * 256, (uint32_t)(c * 64 + lane) * 4u, rs);
+      }
+    }
+  };
+  // its scales, 64 a load
+  auto load_scales = [&](const Tile& o, int par) __attribute__((always_inline)) {
+    const i32x4 rsSW = make_rsrc(a.SW + (size_t)o.expert * a.C, K > 0 ? (uint32_t)a.C * 4u : 0u);
+#pragma unroll
+    for (int c0 = 0; c0 < (BM + BNW) / 64; c0 += C::kWaves) {
+      const int c = c0 + wave_u;
+      if (c < BM / 64) {
+        const int r = c * 64 + lane;
+        int row = r < o.rows ? o.pos0 + r : -1;
+        if constexpr (GROUPED && OP == I8_GATED) {
+          const int slot = reinterpret_cast<const int*>(smem + C::ROW_OFF + par * 4 * BM)[r];
+          row = r < o.rows && slot >= 0 && slot / a.k < a.TA ? slot / a.k : -1;
+        }
+        lds_dma4(lds0 + C::SA_OFF + par * 4 * BM + c * 256, row >= 0 ? (uint32_t)row * 4u : kOutOfRange, rsSA);
+      } else if (c < (BM + BNW) / 64) {
+        const int r = (c - BM / 64) * 64;
+        lds_dma4(lds0 + C::SW_OFF + par * 4 * BNW + r * 4, (uint32_t)(o.tn * BNW + r + lane) * 4u, rsSW);
+      }
+    }
+  };
+
+  // ---- fragments ------------------------------------------------------------------------
+  // A wave's blocks of rows are those j WGM + wm, so a short tile leaves every wave about as many.
+  u32x4 af[2][C::FA], wf[2][C::FW];
+  const int fr = lane & 31, fh = lane >> 5;
+  uint32_t fa = (uint32_t)(wm * 2048 + fr * 64), fw = (uint32_t)(C::A_BYTES + wn * C::FW * 2048 + lane * 16);
+  const uint32_t fc[2] = {(uint32_t)((fh ^ C::swz(fr)) * 16), (uint32_t)(((2 + fh) ^ C::swz(fr)) * 16)};
+  auto frag = [&](uint32_t ba, uint32_t bw, int half, int sub, int r) __attribute__((always_inline)) {
+    const int at = half * C::STAGE;
+    if (r < C::FW)
+      wf[sub][r] = *reinterpret_cast<const u32x4*>(smem + bw + (at + r * 2048 + sub * 1024));
+    else
+      af[sub][r - C::FW] =
+          *reinterpret_cast<const u32x4*>(smem + (ba + fc[sub]) + (at + (r - C::FW) * WGM * 2048));
+  };
+  i32x16 acc[C::FW][C::FA];
+
+  Tile cur = locate(first, 0), nxt = cur;
+  i32x4 w_cur = weights(cur), w_nxt = w_cur;
+  int par = 0;
+
+  // Sub-step B (32 k) of a group.  The even ones read the other sub-step of their stage;
+  // the odd ones wait for the next stage, and behind the barrier (every wave has read this stage)
+  // read the next one's first fragments and load the stage of the group after next in this one's
+  // place.  LIVE: the wave's blocks of rows that the tile has; LAST: the next stage is the next
+  // tile's.
+  auto step = [&](auto b_c, auto live_c, auto last_c, const Tile& o, const i32x4& rsW,
+                  const uint32_t* rows, int g, int lg, int slot) __attribute__((always_inline)) {
+    constexpr int B = decltype(b_c)::value, SUB = B & 1, HALF = B >> 1, LIVE = decltype(live_c)::value;
+    constexpr bool LAST = decltype(last_c)::value && B == 3;
+    constexpr int NMF = C::FW * LIVE, NFRAG = C::FW + (LAST ? C::FA : LIVE);
+    if constexpr (SUB == 1) {
+      wait_vmcnt<2 * C::LOADS>();
+      __syncthreads();
+      if constexpr (B == 1) {
+        if (GROUPED && g == 0 && nxt.rows > 0) load_slots(nxt, par ^ 1);
+        if (g == Gp - 2 && nxt.rows > 0) load_scales(nxt, par ^ 1);
+      }
+    }
+    const int turn = HALF == 1 && SUB == 1 ? (slot ? -C::GROUP : C::GROUP) : 0;
+    const uint32_t na = fa + turn, nw = fw + turn;
+    auto one = [&](auto q_c) __attribute__((always_inline)) {
+      constexpr int Q = decltype(q_c)::value, i = Q / LIVE, j = Q % LIVE;
+      acc[i][j] = mfma32_i8(wf[SUB][i], af[SUB][j], acc[i][j]);
+#pragma unroll
+      for (int r = Q * NFRAG / NMF; r < (Q + 1) * NFRAG / NMF; ++r)
+        frag(na, nw, SUB == 0 ? HALF : HALF ^ 1, SUB ^ 1, r);
+      if constexpr (SUB == 1) {
+#pragma unroll
+        for (int q = Q * C::LOADS / NMF; q < (Q + 1) * C::LOADS / NMF; ++q)
+          dma(o, rsW, rows, lg, slot, HALF, q);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    [&]<int... Q>(std::integer_sequence<int, Q...>) __attribute__((always_inline)) {
+      (one(std::integral_constant<int, Q>{}), ...);
+    }(std::make_integer_sequence<int, NMF>{});
+  };
+
+  // ---- the first tile's slots and scales, its first two groups, the first fragments ------
+  if constexpr (GROUPED) {
+    load_slots(cur, 0);
+    wait_vmcnt<0>();
+    __syncthreads();
+  }
+  load_scales(cur, 0);
+#pragma unroll
+  for (int q = 0; q < C::A_LOADS; ++q) off[q] = a_offset(cur, 0, q);
+#pragma unroll
+  for (int st = 0; st < 4; ++st)
+#pragma unroll
+    for (int q = 0; q < C::LOADS; ++q) dma(cur, w_cur, off, st / 2, st / 2, st % 2, q);
+  wait_vmcnt<3 * C::LOADS>();
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < C::FW + C::FA; ++r) frag(fa, fw, 0, 0, r);
+
+  int slot = 0;
+  for (int t = first; t < end; t += stride) {
+    nxt = locate(t + stride, cur.expert);
+    w_nxt = GROUPED ? weights(nxt) : w_cur;
+#pragma unroll
+    for (int i = 0; i < C::FW; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FA; ++j) acc[i][j] = i32x16{};
+    const int blocks = (cur.rows + 31) / 32;
+    const int live = (blocks - wm + WGM - 1) / WGM;
+    auto groups = [&](auto live_c) __attribute__((always_inline)) {
+      using No = std::integral_constant<bool, false>;
+      using Yes = std::integral_constant<bool, true>;
+      auto group = [&](auto last_c, const Tile& o, const i32x4& rsW, const uint32_t* rows, int g,
+                       int lg) __attribute__((always_inline)) {
+        step(std::integral_constant<int, 0>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
+        step(std::integral_constant<int, 1>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
+        step(std::integral_constant<int, 2>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
+        step(std::integral_constant<int, 3>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
+        const int turn = slot ? -C::GROUP : C::GROUP;
+        fa += turn;
+        fw += turn;
+        slot ^= 1;
+      };
+      int g = 0;
+      for (; g < Gp - 2; ++g) group(No{}, cur, w_cur, off, g, g + 2);
+      // the groups to load are the next tile's
+#pragma unroll
+      for (int q = 0; q < C::A_LOADS; ++q) a_next[q] = a_offset(nxt, par ^ 1, q);
+      group(No{}, nxt, w_nxt, a_next, g, 0);
+      group(Yes{}, nxt, w_nxt, a_next, g + 1, 1);
+    };
+    if (C::FA >= 4 && live >= 4) {
+      if constexpr (C::FA >= 4) groups(std::integral_constant<int, 4>{});
+    } else if (C::FA >= 3 && live >= 3) {
+      if constexpr (C::FA >= 3) groups(std::integral_constant<int, 3>{});
+    } else if (C::FA >= 2 && live >= 2) {
+      if constexpr (C::FA >= 2) groups(std::integral_constant<int, 2>{});
+    } else {
+      groups(std::integral_constant<int, 1>{});
+    }
+    // Scales, SiLU(Gate) Up, stores.  Registers 4 q .. 4 q + 3 are weight rows 8 q + 4 h + 0
+    // .. 3 (h = lane / 32); the exchanges give a lane 8 output columns next to each other.
+    const float* sa = reinterpret_cast<const float*>(smem + C::SA_OFF + par * 4 * BM);
+    const uint8_t* sw = smem + C::SW_OFF + par * 4 * BNW;
+    const int* slots = reinterpret_cast<const int*>(smem + C::ROW_OFF + par * 4 * BM);
+#pragma unroll
+    for (int j = 0; j < C::FA; ++j) {
+      const int r = (j * WGM + wm) * 32 + fr;
+      if ((j * WGM + wm) * 32 >= cur.rows) continue;  // as a wave
+      const float s = sa[r];
+      int row = cur.pos0 + r;
+      if constexpr (GROUPED && OP == I8_PLAIN) row = slots[r];
+      const bool there = r < cur.rows && row >= 0 && row < a.R;
+      uint16_t* y = a.Y + (size_t)(there ? row : 0) * a.N;
+#pragma unroll
+      for (int i = 0; i < C::FW; ++i) {
+        const i32x16& d = acc[i][j];
+        float p[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 c = *reinterpret_cast<const f32x4*>(sw + ((wn * C::FW + i) * 32 + 8 * q + 4 * fh) * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[4 * q + e] = (float)d[4 * q + e] * s * c[e];
+        }
+        if constexpr (OP == I8_GATED) {
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            o[q] = pack_bf16x2(silu(p[4 * q]) * p[4 * q + 1], silu(p[4 * q + 2]) * p[4 * q + 3]);
+          swap_halves(o[0], o[2]);
+          swap_halves(o[1], o[3]);
+          const int col = (cur.tn * C::NW + wn * C::FW + i) * 16 + 8 * fh;
+          if (there && col < a.N) *reinterpret_cast<u32x4*>(y + col) = u32x4{o[0], o[2], o[1], o[3]};
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(p[4 * q + 2 * e], p[4 * q + 2 * e + 1]);
+            swap_halves(o[0], o[2]);
+            swap_halves(o[1], o[3]);
+            const int col = (cur.tn * C::NW + wn * C::FW + i) * 32 + 8 * (q + fh);
+            if (there && col < a.N) *reinterpret_cast<u32x4*>(y + col) = u32x4{o[0], o[1], o[2], o[3]};
+          }
+        }
+      }
+    }
+    cur = nxt;
+    w_cur = w_nxt;
+#pragma unroll
+    for (int q = 0; q < C::A_LOADS; ++q) off[q] = a_next[q];
+    par ^= 1;
+  }
+  // the zero loads issued past the last tile still write LDS
+  wait_vmcnt<0>();
+}
+
+// ============================================================================
 // Few rows: weight streaming
 // ============================================================================
 // A workgroup takes NB blocks of 32 weight rows and MT blocks of 32 activation rows
@@ -338,15 +700,47 @@ static hipError_t launch_int8_stream(const Int8Call& c, const Int8Args& g, hipSt
                    dim3((unsigned)nblk, (unsigned)nmb), dim3(64 * NW), stream, g, (int)nblk);
 }
 
+template <int BM, int BNW, int WGM, int WGN>
+static long long int8_tile_grid(const Int8Call& c) {
+  using T = Int8Tile<BM, BNW, WGM, WGN>;
+  const long long tiles = int8_row_tiles(c, BM) * ((c.C() + BNW - 1) / BNW);
+  // eight at least: each XCD's range of tiles needs a workgroup there.  By expert an eighth of
+  // the work may be more than an eighth of the tiles, hence all that the device holds.
+  const long long most = std::max<long long>((long long)c.cu_count * T::kPerCu, 8);
+  return std::min(c.grouped ? (2 * tiles + 7) / 8 * 8 : tiles, most);
+}
+template <int OP, bool GROUPED, int BM, int BNW, int WGM, int WGN, int PARTS>
+static hipError_t launch_int8_tile(const Int8Call& c, const Int8Args& g, hipStream_t stream) {
+  const long long ntn = (c.C() + BNW - 1) / BNW;
+  if (int8_row_tiles(c, BM) * ntn > 0x7fffffffLL) return hipErrorInvalidValue;
+  const int group_m = GROUPED ? 8 : 4;
+  return launch_op(int8_tile_kernel<OP, GROUPED, BM, BNW, WGM, WGN, PARTS>,
+                   dim3((unsigned)int8_tile_grid<BM, BNW, WGM, WGN>(c)), dim3(64 * WGM * WGN), stream,
+                   g, (int)ntn, group_m);
+}
+
+static int int8_variant(const Int8Call& c) {
+  const long long some = std::min(c.R, c.E), mean = c.grouped ? (c.R + some - 1) / some : c.R;
+  if (mean <= 32) return 0;
+  if (mean <= 64) return 1;
+  const long long large = int8_row_tiles(c, 256) * ((c.C() + 255) / 256);
+  return large < c.cu_count ? 2 : 3;
+}
+
 template <int OP, bool GROUPED>
 static hipError_t launch_int8_as(const Int8Call& c, int variant, hipStream_t stream) {
   const Int8Args g{c.A,        c.SA,     c.rows,   c.offsets, c.W,      c.SW,     c.Y,       (int)c.TA,
                    (int)c.R,   (int)c.N, (int)c.K, (int)c.E,  (int)c.k, (int)c.C()};
-  (void)variant;
-  return launch_int8_stream<OP, GROUPED, 1, 1, 4>(c, g, stream);
+  switch (variant) {
+    case 0: return launch_int8_stream<OP, GROUPED, 1, 1, 4>(c, g, stream);
+    case 1: return launch_int8_stream<OP, GROUPED, 2, 1, 4>(c, g, stream);
+    case 2: return launch_int8_tile<OP, GROUPED, 128, 128, 2, 2, 2>(c, g, stream);
+    default: return launch_int8_tile<OP, GROUPED, 256, 256, 2, 4, 4>(c, g, stream);
+  }
 }
 
 hipError_t launch_int8(const Int8Call& c, int variant, hipStream_t stream) {
+  if (variant < 0) variant = int8_variant(c);
   if (c.grouped)
     return c.gated ? launch_int8_as<I8_GATED, true>(c, variant, stream)
                    : launch_int8_as<I8_PLAIN, true>(c, variant, stream);
@@ -356,9 +750,18 @@ hipError_t launch_int8(const Int8Call& c, int variant, hipStream_t stream) {
 
 // Threads of the launch along x, and its workgroups along y.
 void int8_launch_size(const Int8Call& c, int variant, long long* threads, long long* y) {
-  (void)variant;
-  *y = c.grouped ? 1 : (c.R + 31) / 32;
-  *threads = 256 * (c.grouped ? (int8_stream_units(c, 1, 1) + 7) / 8 * 8 : (c.C() + 31) / 32);
+  if (variant < 0) variant = int8_variant(c);
+  *y = 1;
+  if (variant <= 1) {
+    const int mt = variant == 0 ? 1 : 2;
+    if (!c.grouped) *y = (c.R + 32 * mt - 1) / (32 * mt);
+    *threads = 256 * (c.grouped ? (int8_stream_units(c, mt, 1) + 7) / 8 * 8 : (c.C() + 31) / 32);
+  } else {
+    const long long tile = variant == 2 ? 128 : 256;
+    // tile numbers are 32 bits wide
+    const long long tiles = int8_row_tiles(c, tile) * ((c.C() + tile - 1) / tile);
+    *threads = tiles > 0x7fffffffLL - 4096 ? 1LL << 40 : 0;
+  }
 }
 
 // Waves of a row.

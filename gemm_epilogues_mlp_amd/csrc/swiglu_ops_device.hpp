@@ -187,6 +187,39 @@ __device__ __forceinline__ GroupUnit group_unit(const int32_t* __restrict__ offs
   return u;
 }
 
+// The spans laid out in LDS, for workgroups that look up many units: of expert e the
+// first row lo[e], the rows n[e] and the tiles of BM rows up to and with it, upto[e].  By
+// the first wave; a barrier has to follow.
+struct GroupTable {
+  int *lo, *n, *upto;
+};
+template <int BM>
+__device__ __forceinline__ void group_table(const int32_t* __restrict__ offsets, int E, int R,
+                                            const GroupTable& table) {
+  if (threadIdx.x >= 64) return;
+  int before = 0, reach = 0;
+  for (int c = 0; c < E; c += 64) {
+    int lo, n;
+    group_span(offsets, c, E, R, reach, lo, n);
+    const int incl = wave_scan((n + BM - 1) / BM), e = c + (int)threadIdx.x;
+    if (e < E) {
+      table.lo[e] = lo;
+      table.n[e] = n;
+      table.upto[e] = before + incl;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+}
+// the expert of tile t, which is one of the tiles and not before expert `from`
+__device__ __forceinline__ int group_find(const GroupTable& table, int E, int t, int from) {
+  const int lane = threadIdx.x & 63;
+  int c = from & ~63;
+  for (;; c += 64) {
+    const unsigned long long past = __ballot(c + lane >= E || table.upto[c + lane] > t);
+    if (past) return min(c + __ffsll(past) - 1, E - 1);
+  }
+}
+
 // ---- MXFP4 ------------------------------------------------------------------------
 // v_mfma_scale_f32_32x32x64_f8f6f4 with both sources E2M1 (format 4): lane l
 // holds row or column l % 32 and the 32 consecutive k of half l / 32 in 16
@@ -234,6 +267,17 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ i32x16 mfma32_i8(const u32x4& a, const u32x4& b, const i32x16& c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
                                                __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// As lds_dma16 with 4 bytes a lane, at lds_wave_base + 4 lane.
+__device__ __forceinline__ void lds_dma4(uint32_t lds_wave_base, uint32_t voffset, i32x4 rsrc) {
+  lds_wave_base = __builtin_amdgcn_readfirstlane(lds_wave_base);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rsrc[i] = __builtin_amdgcn_readfirstlane(rsrc[i]);
+  asm volatile("buffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voffset), "s"(rsrc), "{m0}"(lds_wave_base)
+               : "memory");
 }
 
 // ---- launches ---------------------------------------------------------------------

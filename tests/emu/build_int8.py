@@ -1,7 +1,9 @@
 """Build the CPU bounds and LDS-ordering emulation of the 8-bit integer kernels
 (host clang++ with AddressSanitizer) from their current source.  Returns the binary
-path.  The rewrites are those of build_ops.py; the planted mistakes are off unless the
-driver is run with --plant N."""
+path.  The rewrites are those of build_ops.py, and one more: the threads of a workgroup run
+one after another, so a slot that another wave's DMA brings is not there yet; its LDS read is
+logged and its value taken from memory.  The planted mistakes are off unless the driver is
+run with --plant N."""
 import os
 import re
 import shutil
@@ -11,6 +13,12 @@ import build as emu_build
 
 HERE, CSRC = emu_build.HERE, emu_build.CSRC
 NAME = "swiglu_int8.hip"
+SLOTS = [
+    (r"const int slot = (reinterpret_cast<const int\*>\(smem \+ C::ROW_OFF \+ par \* 4 \* BM\)\[r\]);",
+     r"const int there = \1; ::emu_use(&there, 4); const int slot = r < o.rows ? a.rows[o.pos0 + r] : -1;", 2),
+    (r"row = slots\[r\];",
+     r"{ const int there = slots[r]; ::emu_use(&there, 4); row = r < cur.rows ? a.rows[cur.pos0 + r] : -1; }", 1),
+]
 PLANTS = []
 
 
@@ -22,6 +30,10 @@ def rewrite(src: str) -> str:
     src = src.replace('#include "swiglu_ops_device.hpp"', '#include "int8_device.hpp"')
     if "__shared__" in src or "asm volatile" in src or "hipLaunchKernel" in src:
         raise RuntimeError(f"{NAME}: a construct the emulation does not rewrite")
+    for pattern, repl, count in SLOTS:
+        src, n = re.subn(pattern, repl, src)
+        if n != count:
+            raise RuntimeError(f"{NAME}: slots read {n} times: {pattern}")
     for pattern, repl in PLANTS:
         src, n = re.subn(pattern, repl, src, flags=re.M)
         if n != 1:

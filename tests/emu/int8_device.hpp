@@ -36,4 +36,25 @@ inline void lds_dma4(uint32_t lds_wave_base, uint32_t voffset, i32x4 rsrc) {
   emu_copy(d, base + voffset, 4);
 }
 
+// the spans' table written out for one thread, and the search in it
+struct GroupTable {
+  int *lo, *n, *upto;
+};
+template <int BM>
+inline void group_table(const int32_t* offsets, int E, int R, const GroupTable& table) {
+  if (threadIdx.x != 0) return;
+  int tiles = 0;
+  for_spans(offsets, E, R, [&](int e, int lo, int n) {
+    tiles += (n + BM - 1) / BM;
+    table.lo[e] = lo;
+    table.n[e] = n;
+    table.upto[e] = tiles;
+  });
+}
+inline int group_find(const GroupTable& table, int E, int t, int from) {
+  int e = from & ~63;
+  while (e < E - 1 && table.upto[e] <= t) ++e;
+  return e;
+}
+
 }  // namespace swiglu

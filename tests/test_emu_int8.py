@@ -14,6 +14,19 @@ DENSE = [("dense", gated, v, m, n, k) for gated in (1, 0) for v in range(5)
          for m, n, k in ((1, 8, 16), (70, 72, 80), (300, 136, 544), (33, 264, 0))]
 GROUPED = [("grouped", gated, v, n, k, 3, 5, c) for gated in (1, 0) for v in range(5)
            for n, k in ((72, 80), (264, 208), (8, 0)) for c in COUNTS]
+# 8 workgroups for all tiles: the ring runs on from one to the next, with 1 to 9 groups of K (run
+# as 2 or 4 at least), an odd number of them too (the ring's halves change places), and
+# spans whose last tiles have every height
+WALKS = [("--cus", 8, "dense", gated, v, 900, 648, k) for gated in (1, 0) for v in (2, 3, 4)
+         for k in (16, 272, 1040)] + \
+    [("--cus", 8, "grouped", gated, v, 264, k, 3, 5, "300,1,0,600,140,70") for gated in (1, 0)
+     for v in (2, 3, 4) for k in (16, 528, 656, 1040)]
+# a device of fewer CUs than the eight ranges that the tiles are dealt out in
+FEW = [("--cus", c, *job) for c in (1, 3) for job in (("dense", 1, 3, 900, 648, 272),
+                                                      ("grouped", 0, 2, 264, 144, 3, 5, "300,1,0,600"))]
+# more than 64 experts: the spans' table is searched in parts
+MANY = [("--cus", 8, "grouped", gated, v, 40, 144, 2, 3, ",".join(["2"] * 70 + ["0"] * 70 + ["70"] * 9))
+        for gated in (1, 0) for v in range(5)]
 OTHER = [("quantize", rows, k) for rows, k in ((5, 16), (6, 1024), (3, 1040), (2, 9008), (2, 20000), (2, 40000))] + \
     [("pack", *a) for a in ((1, 1, 16), (3, 40, 144), (2, 64, 256))]
 
@@ -32,7 +45,7 @@ def runs(tmp_path_factory):
         r = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=300, env=env)
         return r.returncode, r.stdout + r.stderr
     with cf.ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
-        jobs = DENSE + GROUPED + OTHER
+        jobs = DENSE + GROUPED + WALKS + FEW + MANY + OTHER
         yield dict(zip(jobs, ex.map(run, jobs)))
 
 
@@ -48,6 +61,18 @@ def test_dense_launches(runs):
 
 def test_grouped_launches(runs):
     clean(runs, GROUPED)
+
+
+def test_workgroups_walk_over_tiles(runs):
+    clean(runs, WALKS)
+
+
+def test_few_compute_units(runs):
+    clean(runs, FEW)
+
+
+def test_many_experts(runs):
+    clean(runs, MANY)
 
 
 def test_quantisation_and_packing(runs):
