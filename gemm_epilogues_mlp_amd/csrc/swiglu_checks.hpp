@@ -257,9 +257,7 @@ inline int int8_product(const Int8Call& c, int variant, bool* noop) {
   const long long ybytes = mul(c.R, 2 * c.N), wall = mul(c.E, wbytes);
   if (abytes >= kMax2G || wbytes >= kMax2G || wall > kMaxTotal || ybytes > kMaxTotal)
     return kUnsupported;
-  long long threads, y;
-  int8_launch_size(c, variant, &threads, &y);
-  if (threads > kMaxThreads || y > 65535) return kUnsupported;
+  if (!int8_launchable(c, variant)) return kUnsupported;
   const long long some = c.K > 0 ? 1 : 0;  // no scales are read where there is nothing to scale
   if (clash({{c.Y, ybytes}},
             {{c.A, abytes}, {c.SA, some * 4 * c.TA}, {c.W, wall}, {c.SW, some * 4 * c.E * c.C()},

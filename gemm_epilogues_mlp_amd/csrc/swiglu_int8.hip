@@ -16,6 +16,7 @@
 #include "swiglu_ops_device.hpp"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 #include <utility>
 
@@ -325,12 +326,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, i
     const bool in = g < G && o.rows > 0;
     const uint32_t base = lds0 + slot * C::GROUP + half * C::STAGE;
     if (q < C::A_LOADS) {
-      lds_dma16(base + (q * C::kWaves + wave_u) * 1024,
+      lds_dma16_wait(base + (q * C::kWaves + wave_u) * 1024,
                 in ? rows[q] + (uint32_t)(g * 128 + half * 64) : kOutOfRange, rsA);
     } else {
       const uint32_t at = (uint32_t)(o.tn * C::NW) * (uint32_t)G * 4096u + (uint32_t)g * 4096u +
                           (uint32_t)half * 2048u;
-      lds_dma16(base + C::A_BYTES + ((q - C::A_LOADS) * C::kWaves + wave_u) * 1024,
+      lds_dma16_wait(base + C::A_BYTES + ((q - C::A_LOADS) * C::kWaves + wave_u) * 1024,
                 off[q] + (in ? at : kOutOfRange), rsW);
     }
   };
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, i
 #pragma unroll
       for (int c0 = 0; c0 < BM / 64; c0 += C::kWaves) {
         const int c = c0 + wave_u;
-        if (c < BM / 64) lds_dma4(lds0 + C::ROW_OFF + par * 4 * BM + c * 256, (uint32_t)(c * 64 + lane) * 4u, rs);
+        if (c < BM / 64) lds_dma4_wait(lds0 + C::ROW_OFF + par * 4 * BM + c * 256, (uint32_t)(c * 64 + lane) * 4u, rs);
       }
     }
   };
@@ -358,10 +359,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, i
           const int slot = reinterpret_cast<const int*>(smem + C::ROW_OFF + par * 4 * BM)[r];
           row = r < o.rows && slot >= 0 && slot / a.k < a.TA ? slot / a.k : -1;
         }
-        lds_dma4(lds0 + C::SA_OFF + par * 4 * BM + c * 256, row >= 0 ? (uint32_t)row * 4u : kOutOfRange, rsSA);
+        lds_dma4_wait(lds0 + C::SA_OFF + par * 4 * BM + c * 256, row >= 0 ? (uint32_t)row * 4u : kOutOfRange, rsSA);
       } else if (c < (BM + BNW) / 64) {
         const int r = (c - BM / 64) * 64;
-        lds_dma4(lds0 + C::SW_OFF + par * 4 * BNW + r * 4, (uint32_t)(o.tn * BNW + r + lane) * 4u, rsSW);
+        lds_dma4_wait(lds0 + C::SW_OFF + par * 4 * BNW + r * 4, (uint32_t)(o.tn * BNW + r + lane) * 4u, rsSW);
       }
     }
   };
@@ -543,86 +544,93 @@ __global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, i
 // ============================================================================
 // Few rows: weight streaming
 // ============================================================================
-// A workgroup takes NB blocks of 32 weight rows and MT blocks of 32 activation rows
-// (D = W A^T, so that a Gate / Up pair is two adjacent registers of a lane); its NW
-// waves take every NW-th group of 128 k, the next group's loads issued before
-// this one's products. The waves' sums are added in LDS: integers, so their order does
-// not matter.
-template <int OP, bool GROUPED, int MT, int NB, int NW>
+// A workgroup takes NB half blocks of 16 weight rows and MT times 16 rows of A, as D = W A^T on
+// v_mfma_i32_16x16x64_i8 (a Gate / Up pair is two adjacent registers of a lane; rows of
+// A come in 64-byte pieces).  Its NW waves take every NW-th group of 128 k, D groups in
+// flight while one is multiplied.  The waves' sums are added in LDS: integers, so their order
+// does not matter.
+template <int OP, bool GROUPED, int MT, int NB, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void int8_stream_kernel(Int8Args g, int nblk) {
-  constexpr int NQ = MT * NB * 4;
-  __shared__ __attribute__((aligned(16))) i32x4 red[NW > 1 ? NW * NQ * 64 : 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
+  constexpr int BM = 16 * MT;
+  __shared__ __attribute__((aligned(16))) i32x4 red[NW > 1 ? NW * MT * NB * 64 : 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
   const int K = g.K, G = (K + 127) / 128, B = (g.C + 31) / 32;
   int blk, pos0, nrows, expert = 0;
   if constexpr (GROUPED) {
-    const GroupRange range = group_range<32 * MT, 1>(g.offsets, g.E, g.R, nblk, blockIdx.x % 8);
+    const GroupRange range = group_range<BM, 1>(g.offsets, g.E, g.R, nblk, blockIdx.x % 8);
     const int t = range.begin + (int)blockIdx.x / 8;
     if (t >= range.end) return;
-    const GroupUnit u = group_unit<32 * MT>(g.offsets, g.E, g.R, nblk, t);
+    const GroupUnit u = group_unit<BM>(g.offsets, g.E, g.R, nblk, t);
     blk = u.local % nblk;
-    pos0 = u.first + u.local / nblk * (32 * MT);
-    nrows = min(u.first + u.rows - pos0, 32 * MT);
+    pos0 = u.first + u.local / nblk * BM;
+    nrows = min(u.first + u.rows - pos0, BM);
     expert = u.expert;
   } else {
     blk = xcd_remap(blockIdx.x, gridDim.x);
-    pos0 = blockIdx.y * (32 * MT);
-    nrows = min(g.R - pos0, 32 * MT);
+    pos0 = blockIdx.y * BM;
+    nrows = min(g.R - pos0, BM);
   }
   const uint8_t* wp[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)  // a block past the last repeats it; never stored
-    wp[b] = g.W + ((size_t)expert * B + min(blk * NB + b, B - 1)) * G * 4096 + lane * 16;
-  // this lane's rows of A; rows past the span repeat the last one and are never stored
+  for (int b = 0; b < NB; ++b) {  // a half block past the last repeats it; never stored
+    const int half = min(blk * NB + b, 2 * B - 1);
+    wp[b] = g.W + ((size_t)expert * B + (half >> 1)) * G * 4096 +
+            ((quarter >> 1) * 1024 + (quarter & 1) * 512 + (half & 1) * 256 + l16 * 16);
+  }
+  // rows past the span repeat the last one and are never stored
   const uint8_t* ap[MT];
   int ar[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    const int pos = pos0 + min(32 * j + (lane & 31), nrows - 1);
+    const int pos = pos0 + min(16 * j + l16, nrows - 1);
     ar[j] = GROUPED ? int8_a_row<OP>(g, pos) : pos;
-    ap[j] = g.A + (size_t)max(ar[j], 0) * K + 16 * h;
+    ap[j] = g.A + (size_t)max(ar[j], 0) * K + 16 * quarter;
   }
-  i32x16 acc[MT][NB];
+  i32x4 acc[MT][NB];
 #pragma unroll
   for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[j][b] = i32x16{};
+    for (int b = 0; b < NB; ++b) acc[j][b] = i32x4{0, 0, 0, 0};
 
-  u32x4 w[2][NB][4], a[2][MT][4];
-  auto load = [&](int p, int gi) __attribute__((always_inline)) {
+  u32x4 w[D + 1][NB][2], a[D + 1][MT][2];
+  auto load = [&](auto p_c, int gi) __attribute__((always_inline)) {
+    constexpr int P = decltype(p_c)::value;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) w[p][b][s] = load16_stream(wp[b] + (size_t)gi * 4096 + s * 1024);
+      for (int s = 0; s < 2; ++s) w[P][b][s] = load16_stream(wp[b] + (size_t)gi * 4096 + s * 2048);
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int k = gi * 128 + s * 32;
-        a[p][j][s] = k + 16 * h < K && ar[j] >= 0 ? load16(ap[j] + k) : u32x4{0, 0, 0, 0};
+      for (int s = 0; s < 2; ++s) {
+        const int k = gi * 128 + s * 64;
+        a[P][j][s] = k + 16 * quarter < K && ar[j] >= 0 ? load16(ap[j] + k) : u32x4{0, 0, 0, 0};
       }
   };
-  auto multiply = [&](int p) __attribute__((always_inline)) {
+  // round P of D + 1: this wave's group gi, and the load of the one D rounds on in the
+  // registers that the round before has used
+  auto round = [&](auto p_c, int gi) __attribute__((always_inline)) {
+    constexpr int P = decltype(p_c)::value;
+    if (gi >= G) return;
+    if (gi + D * NW < G) load(std::integral_constant<int, (P + D) % (D + 1)>{}, gi + D * NW);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) acc[j][b] = mfma32_i8(w[p][b][s], a[p][j][s], acc[j][b]);
+        for (int b = 0; b < NB; ++b) acc[j][b] = mfma16_i8(w[P][b][s], a[P][j][s], acc[j][b]);
   };
-  int gi = wave;
-  if (gi < G) load(0, gi);
-  for (; gi < G; gi += 2 * NW) {
-    if (gi + NW < G) load(1, gi + NW);
-    multiply(0);
-    if (gi + NW >= G) break;
-    if (gi + 2 * NW < G) load(0, gi + 2 * NW);
-    multiply(1);
-  }
+  [&]<int... P>(std::integer_sequence<int, P...>) __attribute__((always_inline)) {
+    ((wave + P * NW < G ? (load(std::integral_constant<int, P>{}, wave + P * NW), 0) : 0), ...);
+  }(std::make_integer_sequence<int, D>{});
+  for (int gi = wave; gi < G; gi += (D + 1) * NW)
+    [&]<int... P>(std::integer_sequence<int, P...>) __attribute__((always_inline)) {
+      (round(std::integral_constant<int, P>{}, gi + P * NW), ...);
+    }(std::make_integer_sequence<int, D + 1>{});
 
-  // quarter q of a lane: weight rows 32 block + 8 q + 4 h + 0 .. 3 of A's row lane % 32
-  auto store = [&](int j, int b, int q, const i32x4& v) __attribute__((always_inline)) {
-    const int row = 32 * j + (lane & 31), c = (blk * NB + b) * 32 + 8 * q + 4 * h;
+  // register r: weight row 16 half + 4 quarter + r of A's row lane % 16
+  auto store = [&](int j, int b, const i32x4& v) __attribute__((always_inline)) {
+    const int row = 16 * j + l16, c = (blk * NB + b) * 16 + 4 * quarter;
     if (row >= nrows || c >= g.C) return;
     const float sa = K > 0 && ar[j] >= 0 ? g.SA[ar[j]] : 0.0f;
     f32x4 sw{0, 0, 0, 0};
@@ -642,23 +650,11 @@ __global__ __launch_bounds__(64 * NW) void int8_stream_kernel(Int8Args g, int nb
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const i32x16& d = acc[j][b];
-          store(j, b, q, i32x4{d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]});
-        }
+      for (int b = 0; b < NB; ++b) store(j, b, acc[j][b]);
   } else {
+    constexpr int NQ = MT * NB;
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const i32x16& d = acc[j][b];
-          red[(wave * NQ + (j * NB + b) * 4 + q) * 64 + lane] =
-              i32x4{d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
-        }
+    for (int x = 0; x < NQ; ++x) red[(wave * NQ + x) * 64 + lane] = acc[x / NB][x % NB];
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
@@ -666,7 +662,7 @@ __global__ __launch_bounds__(64 * NW) void int8_stream_kernel(Int8Args g, int nb
       i32x4 v = red[x * 64 + lane];
 #pragma unroll
       for (int o = 1; o < NW; ++o) v += red[(o * NQ + x) * 64 + lane];
-      store(x / 4 / NB, x / 4 % NB, x % 4, v);
+      store(x / NB, x % NB, v);
     }
   }
 }
@@ -681,23 +677,14 @@ static long long int8_row_tiles(const Int8Call& c, long long bm) {
   const long long some = std::min(c.R, c.E);
   return std::min(c.R, (c.R + some * (bm - 1)) / bm);
 }
-static long long int8_stream_units(const Int8Call& c, int mt, int nb) {
-  return int8_row_tiles(c, 32 * mt) * ((c.C() + 32 * nb - 1) / (32 * nb));
-}
-
-template <int OP, bool GROUPED, int MT, int NB, int NW>
+template <int OP, bool GROUPED, int MT, int NB, int NW, int D>
 static hipError_t launch_int8_stream(const Int8Call& c, const Int8Args& g, hipStream_t stream) {
-  const long long nblk = (c.C() + 32 * NB - 1) / (32 * NB);
-  if (GROUPED) {
-    const long long grid = (int8_stream_units(c, MT, NB) + 7) / 8 * 8;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-    return launch_op(int8_stream_kernel<OP, GROUPED, MT, NB, NW>, dim3((unsigned)grid),
-                     dim3(64 * NW), stream, g, (int)nblk);
-  }
-  const long long nmb = (c.R + 32 * MT - 1) / (32 * MT);
-  if (nblk > 0x7fffffffLL || nmb > 65535) return hipErrorInvalidValue;
-  return launch_op(int8_stream_kernel<OP, GROUPED, MT, NB, NW>,
-                   dim3((unsigned)nblk, (unsigned)nmb), dim3(64 * NW), stream, g, (int)nblk);
+  const long long nblk = (c.C() + 16 * NB - 1) / (16 * NB), tiles = int8_row_tiles(c, 16 * MT);
+  // all units weigh the same, so no XCD has more than an eighth of them, rounded up
+  const long long x = GROUPED ? (tiles * nblk + 7) / 8 * 8 : nblk, y = GROUPED ? 1 : tiles;
+  if (x > 0x7fffffffLL || y > 65535) return hipErrorInvalidValue;
+  return launch_op(int8_stream_kernel<OP, GROUPED, MT, NB, NW, D>, dim3((unsigned)x, (unsigned)y),
+                   dim3(64 * NW), stream, g, (int)nblk);
 }
 
 template <int BM, int BNW, int WGM, int WGN>
@@ -712,29 +699,110 @@ static long long int8_tile_grid(const Int8Call& c) {
 template <int OP, bool GROUPED, int BM, int BNW, int WGM, int WGN, int PARTS>
 static hipError_t launch_int8_tile(const Int8Call& c, const Int8Args& g, hipStream_t stream) {
   const long long ntn = (c.C() + BNW - 1) / BNW;
-  if (int8_row_tiles(c, BM) * ntn > 0x7fffffffLL) return hipErrorInvalidValue;
   const int group_m = GROUPED ? 8 : 4;
   return launch_op(int8_tile_kernel<OP, GROUPED, BM, BNW, WGM, WGN, PARTS>,
                    dim3((unsigned)int8_tile_grid<BM, BNW, WGM, WGN>(c)), dim3(64 * WGM * WGN), stream,
                    g, (int)ntn, group_m);
 }
 
+// The kernel variants: rows of A and weight rows of a workgroup's piece, workgroups a CU of
+// the tiled ones (0: streaming), and what the choice between them goes by: microseconds of a
+// launch and of a piece beside its loads, bytes a microsecond that a CU takes in with this
+// kernel (both operands, from HBM or an L2) and that all of them take of the weights.
+// Fitted to 90 calls of 1 to 21264 rows, dense and on 4 to 96 experts (each timed in
+// every variant): the choice is 1.6 % off the fastest in the mean, 30 % once (223 rows on 8
+// experts, 1200 x 1712: 10.5 us for the 64 x 128 tile, 8.1 streaming), 19 % at 764 x 728 x 6736
+// (26.7 and 22.4).
+struct Int8Plan {
+  int bm, bn, per_cu;
+  double launch, piece, cu_rate, weight_rate;
+};
+constexpr Int8Plan kInt8Plans[kInt8Variants] = {
+    {16, 16, 0, 3.8, 1.1, 47700, 6.6e6},  {16, 32, 0, 3.4, 0.9, 47800, 6.4e6},
+    {32, 32, 0, 3.3, 0.8, 36800, 4.8e6},  {64, 64, 0, 3.3, 0.2, 31700, 3.2e6},
+    {64, 128, 2, 3.1, 0.4, 59000, 4.6e6}, {128, 128, 2, 4.0, 0.1, 55100, 3.9e6},
+    {128, 256, 1, 2.7, 0.3, 44900, 3.9e6}, {256, 256, 1, 2.1, 1.8, 38500, 5.9e6},
+};
+// Rows of an expert that has any, in the mean (the counts are on the device), and the pieces.
+static long long int8_mean(const Int8Call& c, long long* some) {
+  *some = c.grouped ? std::min(c.R, c.E) : 1;
+  return (c.R + *some - 1) / *some;
+}
+static long long int8_pieces(const Int8Call& c, const Int8Plan& p) {
+  long long some;
+  const long long mean = int8_mean(c, &some);
+  return some * ((mean + p.bm - 1) / p.bm) * ((c.C() + p.bn - 1) / p.bn);
+}
+// Waves along K of a streaming workgroup: enough of them for the device (8, 4 and 2 waves at
+// 16 x 18944 x 3584 plain: 16.8, 20.1, 32.8 us; 32 rows on 64 experts, 3584 x 1536 gated: 45.3,
+// 30.4, 29.2).
+static int int8_waves(const Int8Call& c, const Int8Plan& p) {
+  const long long n = int8_pieces(c, p);
+  return n >= 1024 ? 2 : (n >= 256 ? 4 : 8);
+}
+static double int8_cost(const Int8Call& c, const Int8Plan& p) {
+  long long some;
+  const long long mean = int8_mean(c, &some), tall = (mean + p.bm - 1) / p.bm;
+  const double cus = std::max(c.cu_count, 1);
+  long long rows = (mean + tall - 1) / tall, groups = (c.K + 127) / 128;
+  const double n = (double)int8_pieces(c, p);
+  double t;
+  if (p.per_cu == 0) {
+    t = std::max(n / cus, 1.0) * (double)((rows + p.bn) * groups * 128) / p.cu_rate + p.piece;
+  } else {
+    rows = (rows + 31) / 32 * 32;
+    groups = std::max(groups, c.grouped ? 4LL : 2LL);
+    const double rounds = std::ceil(n / (cus * p.per_cu));
+    const double here = std::min<double>(p.per_cu, std::ceil(n / (cus * rounds)));
+    t = rounds * ((double)((rows + p.bn) * groups * 128) * here / p.cu_rate + p.piece);
+  }
+  return p.launch + std::max(t, (double)(some * c.C()) * (double)c.K / p.weight_rate);
+}
+// Threads of a launch along x, and its workgroups along y; the tiled ones' grids are small, but
+// their tile numbers are 32 bits wide.
+static bool int8_fits(const Int8Call& c, int variant) {
+  const Int8Plan& p = kInt8Plans[variant];
+  const __int128 pieces = (__int128)int8_row_tiles(c, p.bm) * ((c.C() + p.bn - 1) / p.bn);
+  if (p.per_cu) return pieces <= 0x7fffffffLL - 4096;
+  if (!c.grouped && int8_row_tiles(c, p.bm) > 65535) return false;
+  return (c.grouped ? pieces + 7 : (__int128)((c.C() + p.bn - 1) / p.bn)) * 512 < ((__int128)1 << 32);
+}
 static int int8_variant(const Int8Call& c) {
-  const long long some = std::min(c.R, c.E), mean = c.grouped ? (c.R + some - 1) / some : c.R;
-  if (mean <= 32) return 0;
-  if (mean <= 64) return 1;
-  const long long large = int8_row_tiles(c, 256) * ((c.C() + 255) / 256);
-  return large < c.cu_count ? 2 : 3;
+  int best = kInt8Variants - 1;
+  double least = 0;
+  for (int v = kInt8Variants - 1; v >= 0; --v) {
+    if (!int8_fits(c, v)) continue;
+    const double t = int8_cost(c, kInt8Plans[v]);
+    if (least == 0 || t < least) best = v, least = t;
+  }
+  return best;
+}
+bool int8_launchable(const Int8Call& c, int variant) {
+  return int8_fits(c, variant < 0 ? int8_variant(c) : variant);
 }
 
+template <int OP, bool GROUPED, int MT, int NB>
+static hipError_t launch_int8_waves(const Int8Call& c, const Int8Args& g, const Int8Plan& p,
+                                    hipStream_t stream) {
+  switch (int8_waves(c, p)) {
+    case 2: return launch_int8_stream<OP, GROUPED, MT, NB, 2, 2>(c, g, stream);
+    case 4: return launch_int8_stream<OP, GROUPED, MT, NB, 4, 2>(c, g, stream);
+    default: return launch_int8_stream<OP, GROUPED, MT, NB, 8, 2>(c, g, stream);
+  }
+}
 template <int OP, bool GROUPED>
 static hipError_t launch_int8_as(const Int8Call& c, int variant, hipStream_t stream) {
   const Int8Args g{c.A,        c.SA,     c.rows,   c.offsets, c.W,      c.SW,     c.Y,       (int)c.TA,
                    (int)c.R,   (int)c.N, (int)c.K, (int)c.E,  (int)c.k, (int)c.C()};
+  const Int8Plan& p = kInt8Plans[variant];
   switch (variant) {
-    case 0: return launch_int8_stream<OP, GROUPED, 1, 1, 4>(c, g, stream);
-    case 1: return launch_int8_stream<OP, GROUPED, 2, 1, 4>(c, g, stream);
-    case 2: return launch_int8_tile<OP, GROUPED, 128, 128, 2, 2, 2>(c, g, stream);
+    case 0: return launch_int8_waves<OP, GROUPED, 1, 1>(c, g, p, stream);
+    case 1: return launch_int8_waves<OP, GROUPED, 1, 2>(c, g, p, stream);
+    case 2: return launch_int8_waves<OP, GROUPED, 2, 2>(c, g, p, stream);
+    case 3: return launch_int8_stream<OP, GROUPED, 4, 4, 8, 1>(c, g, stream);
+    case 4: return launch_int8_tile<OP, GROUPED, 64, 128, 2, 2, 1>(c, g, stream);
+    case 5: return launch_int8_tile<OP, GROUPED, 128, 128, 2, 2, 2>(c, g, stream);
+    case 6: return launch_int8_tile<OP, GROUPED, 128, 256, 2, 4, 2>(c, g, stream);
     default: return launch_int8_tile<OP, GROUPED, 256, 256, 2, 4, 4>(c, g, stream);
   }
 }
@@ -746,22 +814,6 @@ hipError_t launch_int8(const Int8Call& c, int variant, hipStream_t stream) {
                    : launch_int8_as<I8_PLAIN, true>(c, variant, stream);
   return c.gated ? launch_int8_as<I8_GATED, false>(c, variant, stream)
                  : launch_int8_as<I8_PLAIN, false>(c, variant, stream);
-}
-
-// Threads of the launch along x, and its workgroups along y.
-void int8_launch_size(const Int8Call& c, int variant, long long* threads, long long* y) {
-  if (variant < 0) variant = int8_variant(c);
-  *y = 1;
-  if (variant <= 1) {
-    const int mt = variant == 0 ? 1 : 2;
-    if (!c.grouped) *y = (c.R + 32 * mt - 1) / (32 * mt);
-    *threads = 256 * (c.grouped ? (int8_stream_units(c, mt, 1) + 7) / 8 * 8 : (c.C() + 31) / 32);
-  } else {
-    const long long tile = variant == 2 ? 128 : 256;
-    // tile numbers are 32 bits wide
-    const long long tiles = int8_row_tiles(c, tile) * ((c.C() + tile - 1) / tile);
-    *threads = tiles > 0x7fffffffLL - 4096 ? 1LL << 40 : 0;
-  }
 }
 
 // Waves of a row.

@@ -188,8 +188,9 @@ struct Int8Call {
   int cu_count;
   long long C() const { return gated ? 2 * N : N; }  // weight rows
 };
-constexpr int kInt8Variants = 5;
-void int8_launch_size(const Int8Call& c, int variant, long long* threads, long long* y);
+constexpr int kInt8Variants = 8;
+// whether the sizes fit the launch of the variant (< 0: of the one that the rule takes)
+bool int8_launchable(const Int8Call& c, int variant);
 hipError_t launch_int8(const Int8Call& c, int variant, hipStream_t stream);
 // threads of the quantising launch
 long long int8_quantize_threads(long long rows, long long K);

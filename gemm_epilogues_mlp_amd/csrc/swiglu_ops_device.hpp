@@ -269,12 +269,33 @@ __device__ __forceinline__ i32x16 mfma32_i8(const u32x4& a, const u32x4& b, cons
                                                __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// As lds_dma16 with 4 bytes a lane, at lds_wave_base + 4 lane.
-__device__ __forceinline__ void lds_dma4(uint32_t lds_wave_base, uint32_t voffset, i32x4 rsrc) {
+// v_mfma_i32_16x16x64_i8: lane l holds row or column l % 16 and the 16 consecutive k
+// of quarter l / 16; the output layout is that of the bf16 16x16x32.
+__device__ __forceinline__ i32x4 mfma16_i8(const u32x4& a, const u32x4& b, const i32x4& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                               __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// Direct loads as lds_dma16, 16 or 4 bytes a lane (at lds_wave_base + 4 lane), for kernels
+// that make resources as they go.  Where the compiler keeps one in vector registers it
+// writes the scalar copy with v_readfirstlane or v_readlane, and a vector memory
+// instruction may read such a scalar five wait states later at the earliest; the compiler
+// does not count them for an instruction inside asm.  (Read too early, a stale base or
+// bound lets a load past the tensor through.)  They also cover the one between M0 and the load.
+__device__ __forceinline__ void lds_dma16_wait(uint32_t lds_wave_base, uint32_t voffset, i32x4 rsrc) {
   lds_wave_base = __builtin_amdgcn_readfirstlane(lds_wave_base);
 #pragma unroll
   for (int i = 0; i < 4; ++i) rsrc[i] = __builtin_amdgcn_readfirstlane(rsrc[i]);
-  asm volatile("buffer_load_dword %0, %1, 0 offen lds"
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(voffset), "s"(rsrc), "{m0}"(lds_wave_base)
+               : "memory");
+}
+__device__ __forceinline__ void lds_dma4_wait(uint32_t lds_wave_base, uint32_t voffset, i32x4 rsrc) {
+  lds_wave_base = __builtin_amdgcn_readfirstlane(lds_wave_base);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rsrc[i] = __builtin_amdgcn_readfirstlane(rsrc[i]);
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
                :
                : "v"(voffset), "s"(rsrc), "{m0}"(lds_wave_base)
                : "memory");

@@ -667,8 +667,9 @@ swiglu_status_t swiglu_quantize_int8(swiglu_handle_t h, const void* X, void* Q, 
  * integers.  K = 0 writes Y = 0 and reads no scales.  N % 8 == 0, N <= 2^23,
  * K % 16 == 0, K < 2^17 (where no sum leaves 32 bits), 16-byte aligned Q, P, SW and Y,
  * SQ aligned to 4 bytes, Q and P under 2 GiB (else UNSUPPORTED); Y [M, N] may be larger
- * and must not overlap an input.  variant < 0: chosen from the sizes; 0 ... 4 force one
- * (tests and tuning), a larger one is INVALID_ARG. */
+ * and must not overlap an input.  variant < 0: chosen from the sizes; 0 ... 7 force one
+ * (tests and tuning; 0 to 3 stream the weights and take up to 65535 times 16, 16, 32 and 64
+ * rows, else UNSUPPORTED), a larger one is INVALID_ARG. */
 swiglu_status_t swiglu_forward_int8(swiglu_handle_t h, const void* Q, const float* SQ,
                                     const void* P, const float* SW, void* Y, int64_t M, int64_t N,
                                     int64_t K, int32_t variant, hipStream_t stream);
@@ -683,7 +684,8 @@ swiglu_status_t swiglu_matmul_int8(swiglu_handle_t h, const void* Q, const float
  * expert e, g and u the products of activation row rows[i] / k of (Q, SQ) [T, K] with expert
  * e's matrix of P (E matrices of 2 N rows) and SW [E, 2 N].  Spans, offsets, slots and rows
  * in no span as there; limits as swiglu_forward_int8 for Q and for one expert's
- * matrix, E <= 1024, a launch of fewer than 2^32 threads (else UNSUPPORTED). */
+ * matrix, E <= 1024, R < 2^31 - 1024, fewer than 2^31 - 4096 pieces of the variant's rows and
+ * columns, and fewer than 2^23 with variants 0 to 3 (else UNSUPPORTED). */
 swiglu_status_t swiglu_grouped_forward_int8(swiglu_handle_t h, const void* Q, const float* SQ,
                                             const int32_t* rows, const int32_t* offsets,
                                             const void* P, const float* SW, void* Y, int64_t T,

@@ -13,9 +13,8 @@ long long route_workspace_bytes(long long T, long long E, long long k) { return 
 long long grouped_threads(bool, long long R, long long, long long, int) { return R; }
 long long norm_threads(long long T, long long) { return T; }
 long long int8_quantize_threads(long long rows, long long) { return rows * 1024; }
-void int8_launch_size(const Int8Call& c, int, long long* threads, long long* y) {
-  *y = c.grouped ? 1 : (c.R + 31) / 32;
-  *threads = (c.grouped ? (c.R / 32 + c.E) * (c.C() / 32 + 1) : c.C() / 32 + 1) * 1024;
+bool int8_launchable(const Int8Call& c, int) {
+  return ((c.R + 31) / 32 + c.E) * ((c.C() + 31) / 32) < (1LL << 60);
 }
 }  // namespace swiglu
 

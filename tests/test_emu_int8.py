@@ -10,23 +10,23 @@ import sys
 import pytest
 
 COUNTS = ["40,1,0,300,17", "0,0", "1,1,1", "16,64,0,33", "384,129"]
-DENSE = [("dense", gated, v, m, n, k) for gated in (1, 0) for v in range(5)
+DENSE = [("dense", gated, v, m, n, k) for gated in (1, 0) for v in range(8)
          for m, n, k in ((1, 8, 16), (70, 72, 80), (300, 136, 544), (33, 264, 0))]
-GROUPED = [("grouped", gated, v, n, k, 3, 5, c) for gated in (1, 0) for v in range(5)
+GROUPED = [("grouped", gated, v, n, k, 3, 5, c) for gated in (1, 0) for v in range(8)
            for n, k in ((72, 80), (264, 208), (8, 0)) for c in COUNTS]
 # 8 workgroups for all tiles: the ring runs on from one to the next, with 1 to 9 groups of K (run
 # as 2 or 4 at least), an odd number of them too (the ring's halves change places), and
 # spans whose last tiles have every height
-WALKS = [("--cus", 8, "dense", gated, v, 900, 648, k) for gated in (1, 0) for v in (2, 3, 4)
+WALKS = [("--cus", 8, "dense", gated, v, 900, 648, k) for gated in (1, 0) for v in (4, 5, 6, 7)
          for k in (16, 272, 1040)] + \
     [("--cus", 8, "grouped", gated, v, 264, k, 3, 5, "300,1,0,600,140,70") for gated in (1, 0)
-     for v in (2, 3, 4) for k in (16, 528, 656, 1040)]
+     for v in (4, 5, 6, 7) for k in (16, 528, 656, 1040)]
 # a device of fewer CUs than the eight ranges that the tiles are dealt out in
-FEW = [("--cus", c, *job) for c in (1, 3) for job in (("dense", 1, 3, 900, 648, 272),
-                                                      ("grouped", 0, 2, 264, 144, 3, 5, "300,1,0,600"))]
+FEW = [("--cus", c, *job) for c in (1, 3) for job in (("dense", 1, 7, 900, 648, 272),
+                                                      ("grouped", 0, 5, 264, 144, 3, 5, "300,1,0,600"))]
 # more than 64 experts: the spans' table is searched in parts
 MANY = [("--cus", 8, "grouped", gated, v, 40, 144, 2, 3, ",".join(["2"] * 70 + ["0"] * 70 + ["70"] * 9))
-        for gated in (1, 0) for v in range(5)]
+        for gated in (1, 0) for v in range(8)]
 OTHER = [("quantize", rows, k) for rows, k in ((5, 16), (6, 1024), (3, 1040), (2, 9008), (2, 20000), (2, 40000))] + \
     [("pack", *a) for a in ((1, 1, 16), (3, 40, 144), (2, 64, 256))]
 

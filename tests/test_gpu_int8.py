@@ -11,7 +11,7 @@ import ops_oracle as O
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
-VARIANTS = [-1, 0, 1, 2, 3, 4]
+VARIANTS = [-1, *range(8)]
 
 
 @pytest.fixture(scope="module")

@@ -110,14 +110,14 @@ def product_cases(M, K):
     return [
         (dict(h=None), INVALID), (dict(Q=None), INVALID), (dict(SQ=None), INVALID),
         (dict(P=None), INVALID), (dict(SW=None), INVALID), (dict(Y=None), INVALID),
-        (dict(N=-8), INVALID), (dict(K=-16), INVALID), (dict(variant=5), INVALID), (dict(N=60), UNSUPPORTED),
+        (dict(N=-8), INVALID), (dict(K=-16), INVALID), (dict(variant=8), INVALID), (dict(N=60), UNSUPPORTED),
         (dict(K=24), UNSUPPORTED), (dict(K=1 << 17), UNSUPPORTED), (dict(K=(1 << 17) - 16), DEVICE),
         (dict(Q=P[0] + 8), UNSUPPORTED), (dict(SQ=P[1] + 2), UNSUPPORTED), (dict(SQ=P[1] + 4), DEVICE),
         (dict(P=P[2] + 8), UNSUPPORTED), (dict(SW=P[3] + 4), UNSUPPORTED), (dict(Y=P[4] + 8), UNSUPPORTED),
         (dict(N=(1 << 23) + 8, K=16), UNSUPPORTED), (dict(N=1 << 20, K=2048), UNSUPPORTED),
         (dict(Y=P[0]), INVALID), (dict(Y=P[1]), INVALID), (dict(Y=P[2]), INVALID), (dict(Y=P[3]), INVALID),
         (dict(N=0, Y=None), OK), (dict(K=0, Q=None, SQ=None, P=None, SW=None), DEVICE),
-        (dict(variant=4), DEVICE)]
+        *((dict(variant=v), DEVICE) for v in range(8))]
 
 
 @pytest.mark.parametrize("name", ["swiglu_forward_int8", "swiglu_matmul_int8"])
@@ -125,7 +125,7 @@ def test_dense_int8(handle, name):
     d = dict(h=handle, Q=P[0], SQ=P[1], P=P[2], SW=P[3], Y=P[4], M=10, N=64, K=64, variant=-1, stream=None)
     check(name, d, product_cases(10, 64) + [
         (dict(M=-1), INVALID), (dict(M=0, Y=None), OK), (dict(M=GIB // 32), UNSUPPORTED),
-        (dict(M=1 << 20), DEVICE), (dict(M=1 << 40), UNSUPPORTED), (dict(M=(1 << 63) - 1), UNSUPPORTED)])
+        (dict(M=GIB // 32 - 1), DEVICE), (dict(M=1 << 40), UNSUPPORTED), (dict(M=(1 << 63) - 1), UNSUPPORTED)])
 
 
 @pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
@@ -144,6 +144,33 @@ def test_grouped_int8(handle, gated):
               (dict(T=GIB // 32 - 1), DEVICE), (dict(T=0, Q=None, SQ=None), DEVICE)] if gated else \
         [(dict(R=GIB // 32), UNSUPPORTED)]
     check("swiglu_grouped_forward_int8" if gated else "swiglu_grouped_matmul_int8", d, cases)
+
+
+def test_int8_launch_size(handle):
+    """What a variant's grid does not hold is refused; the rule takes one that does."""
+    dense, grouped = sw.load().swiglu_forward_int8, sw.load().swiglu_grouped_matmul_int8
+    for v, rows in enumerate((16, 16, 32, 64)):
+        most = 65535 * rows
+        assert dense(handle, P[0], P[1], P[2], P[3], P[4], most, 8, 16, v, None) == DEVICE, v
+        assert dense(handle, P[0], P[1], P[2], P[3], P[4], most + 1, 8, 16, v, None) == UNSUPPORTED, v
+        assert dense(handle, P[0], P[1], P[2], P[3], P[4], most + 1, 8, 16, -1, None) == DEVICE, v
+    for v, (rows, cols) in enumerate(((16, 16), (16, 32), (32, 32), (64, 64))):
+        # one expert: pieces of 512 threads at most, in eights
+        n = 2 ** 11
+        args = (P[0], P[1], P[5], P[6], P[2], P[3], P[4])
+        most = (2 ** 23 // n - 1) * rows
+        assert grouped(handle, *args, most, n * cols, 16, 1, v, None) == DEVICE, v
+        assert grouped(handle, *args, most + 1, n * cols, 16, 1, v, None) == UNSUPPORTED, v
+        assert grouped(handle, *args, most + 1, n * cols, 16, 1, -1, None) == DEVICE, v
+    for v, (rows, cols) in enumerate(((64, 128), (128, 128), (128, 256)), 4):
+        # no K: nothing bounds the rows but the tiles' numbers (and Y's 2^46 bytes)
+        n = 2 ** 23 // cols
+        most = (2 ** 31 - 4097) // n * rows
+        assert most * 2 ** 23 <= 2 ** 46
+        for m, want in ((most, DEVICE), (most + 1, UNSUPPORTED)):
+            assert dense(handle, None, None, None, None, P[4], m, 2 ** 22, 0, v, None) == want, v
+    assert dense(handle, None, None, None, None, P[4], 2 ** 31 - 1025, 8, 0, -1, None) == DEVICE
+    assert dense(handle, None, None, None, None, P[4], 2 ** 31 - 1023, 8, 0, -1, None) == UNSUPPORTED
 
 
 def test_no_size_overflows_a_check(tmp_path):
