@@ -182,132 +182,455 @@ __device__ __forceinline__ void route_token_keys(const RouteArgs& a, int t, bool
 // ---- scored choice -------------------------------------------------------------------
 // swiglu_route_scored: with a score s of each logit (its sigmoid, or the softmax over the
 // open ones) and c = s + bias, the k largest c of the kept groups are chosen, and s is
-// the weight.  Scores, sums and comparisons are in 64 bits: neighbours among some hundred
-// scores between 0 and 1 come as close as fp32 rounds exp, and the choice is to be that
-// of the definition.
+// the weight.  Scores, sums and comparisons are in 64 bits by definition: neighbours among
+// some hundred scores between 0 and 1 come as close as fp32 rounds exp, and the choice is to
+// be that of the definition.  Comparing 64-bit values lane by lane is slow (35.8 us for 8191
+// tokens, 256 experts in 8 groups, against FAST_US), so c is first compared as a
+// whole number, its place between the least and the largest possible value in some 2^28
+// steps.  Two numbers in different steps are in the right order; where two that meet at
+// a choice are not told apart (equal logits, or chance: some 1e-7 a pair), the wave takes
+// the 64-bit path.  Without a bias the logits themselves are in the order of the scores.
 struct NoScore {};
+template <bool SIGMOID_>
+struct Scores : RouteScore {
+  static constexpr bool SIGMOID = SIGMOID_;
+};
+constexpr double kNegInfD = -__builtin_inf();
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);  // no lane is left out
+}
 template <int CTRL>
 __device__ __forceinline__ double dpp_d(double v) {
   const uint64_t x = __builtin_bit_cast(uint64_t, v);
-  const int lo = (int)(uint32_t)x, hi = (int)(uint32_t)(x >> 32);
-  const uint32_t a = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xf, 0xf, false);
-  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xf, 0xf, false);
-  return __builtin_bit_cast(double, (uint64_t)b << 32 | a);
+  return __builtin_bit_cast(double, (uint64_t)dpp_u<CTRL>((uint32_t)(x >> 32)) << 32 |
+                                        dpp_u<CTRL>((uint32_t)x));
+}
+// v of the other row of 16 lanes of a pair, or of the other half wave: both are in a and b
+__device__ __forceinline__ void both_rows(uint32_t v, uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void both_halves(uint32_t v, uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  a = r[0];
+  b = r[1];
 }
 // over aligned groups of G lanes (16, 32 or 64); every lane receives the same bits
+template <int G>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = max(v, dpp_u<kDppXor1>(v));
+  v = max(v, dpp_u<kDppXor2>(v));
+  v = max(v, dpp_u<kDppHalfMirror>(v));
+  v = max(v, dpp_u<kDppMirror>(v));
+  uint32_t a, b;
+  if (G >= 32) both_rows(v, a, b), v = max(a, b);
+  if (G >= 64) both_halves(v, a, b), v = max(a, b);
+  return v;
+}
 template <int G, typename F>
-__device__ __forceinline__ double group_fold(double v, F f) {
+__device__ __forceinline__ double lanes_fold(double v, F f) {
   v = f(v, dpp_d<kDppXor1>(v));
   v = f(v, dpp_d<kDppXor2>(v));
   v = f(v, dpp_d<kDppHalfMirror>(v));
   v = f(v, dpp_d<kDppMirror>(v));
-  if (G >= 32) v = f(v, __shfl_xor(v, 16));
-  if (G >= 64) v = f(v, __shfl_xor(v, 32));
+  auto pair = [&](auto split) __attribute__((always_inline)) {
+    const uint64_t x = __builtin_bit_cast(uint64_t, v);
+    uint32_t lo[2], hi[2];
+    split((uint32_t)x, lo[0], lo[1]);
+    split((uint32_t)(x >> 32), hi[0], hi[1]);
+    v = f(__builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]),
+          __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]));
+  };
+  if (G >= 32) pair(both_rows);
+  if (G >= 64) pair(both_halves);
   return v;
 }
-constexpr double kNegInfD = -__builtin_inf();
 __device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ double sum_of(double a, double b) { return a + b; }
+
+// e^x for x <= 709, within some 2^-52: x = n ln 2 + r with |r| <= ln(2) / 2, the Taylor
+// polynomial of e^r to the 13th power (what is left out is below 2^-57), scaled by 2^n.
+__device__ __forceinline__ double exp_d(double x) {
+  x = x > -760.0 ? x : -760.0;  // 0 from there on
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  // ln 2 as fp32, n times which is exact, and what that leaves of it
+  double r = __builtin_fma(n, -(double)0.6931471805599453f, x);
+  r = __builtin_fma(n, 1.904654299957768e-09, r);
+  double p = 1.0 / 6227020800.0;
+  constexpr double f[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                            1.0 / 40320.0,     1.0 / 5040.0,     1.0 / 720.0,     1.0 / 120.0,
+                            1.0 / 24.0,        1.0 / 6.0,        0.5,             1.0,
+                            1.0};
+#pragma unroll
+  for (int i = 0; i < 13; ++i) p = __builtin_fma(p, r, f[i]);
+  return __builtin_ldexp(p, (int)n);
+}
+// 1 / d for a normal d: the hardware's estimate and two steps of Newton
+__device__ __forceinline__ double reciprocal_d(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+// The score of logit x, but for the division by the sum in a softmax (m its largest logit; an
+// infinite one shares the weight with its equals).  Below -709, where e^-x has no value, the
+// sigmoid is as there.
+template <bool SIGMOID>
+__device__ __forceinline__ double score_of(float x, float m) {
+  if constexpr (SIGMOID) return reciprocal_d(1.0 + exp_d(-(double)fmaxf(x, -709.0f)));
+  constexpr float kMost = 3.402823466e38f;
+  return exp_d((double)fminf(x, kMost) - (double)fminf(m, kMost));
+}
+
+// What stays the same from token to token: the biases of the lane's experts, and the
+// step of a whole number.
+template <int C>
+struct ScoreLane {
+  float bias[C];
+  double steps, first;  // c is in step c steps + first
+};
+constexpr int kScoreBits = 28;
+template <int G, int C>
+__device__ __forceinline__ ScoreLane<C> score_lane(const RouteArgs& a, const RouteScore& sc) {
+  const int gl = threadIdx.x & (G - 1);
+  ScoreLane<C> o;
+  uint32_t most = 0;  // the largest magnitude of a bias that leaves its expert open
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    o.bias[j] = sc.bias ? sc.bias[min(gl * C + j, a.E - 1)] : 0.0f;
+    const uint32_t size = __builtin_bit_cast(uint32_t, o.bias[j]) & 0x7fffffffu;
+    most = max(most, o.bias[j] > kNegInf ? size : 0u);
+  }
+  const double span = (double)__builtin_bit_cast(float, lanes_max<G>(most));
+  // an infinite one tells nothing apart, and every token takes the 64-bit path
+  o.steps = span < 3e38 ? (double)((1 << kScoreBits) - 3) * reciprocal_d(2.0 * span + 1.0) : 0.0;
+  o.first = span * o.steps + 1.5;  // step 0 is that of a closed expert
+  return o;
+}
 
 // LDS of one token.
 template <int N>
 struct ScoreRoom {
   double c[N];             // of all experts
-  double value[kMaxGroups];
-  double picked[64];       // scores of the chosen ones
+  union {
+    uint32_t key[N];       // what stands for c, while groups are compared
+    float x[N];            // then their logits
+  };
+  union {
+    double value[kMaxGroups];
+    uint32_t number[kMaxGroups + 4];
+  };
   int index[64];
 };
+__device__ __forceinline__ void room_written() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();  // other lanes' places: no read moves above this
+}
+
+// whether the groups of the lane's experts are kept, from `room`
+template <int G, int C>
+__device__ __forceinline__ void read_kept(const RouteArgs& a, int size, const ScoreRoom<G * C>& room,
+                                          uint32_t& kept) {
+  const int gl = threadIdx.x & (G - 1);
+  const float by = 1.0f / (float)size;
+  kept = 0;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    // (e + 1/2) / size is 1 / (2 size) or more from a whole number
+    const int e = min(gl * C + j, a.E - 1);
+    kept |= (uint32_t)room.index[(int)(((float)e + 0.5f) * by)] << j;
+  }
+}
+
+// Which of the lane's logits have a group that is kept; false where whole numbers do not tell
+// (or none of the groups has two open experts, whose sum has another zero).
+template <int G, int C>
+__device__ __forceinline__ bool keep_groups(const RouteArgs& a, const RouteScore& sc,
+                                            const uint32_t (&key)[C], bool exact,
+                                            ScoreRoom<G * C>& room, uint32_t& kept) {
+  const int gl = threadIdx.x & (G - 1), size = a.E / sc.groups, lanes = size / C;
+  const bool two = sc.group_best == 2;
+  bool sure = true;
+  auto value = [&](uint32_t first, uint32_t second) __attribute__((always_inline)) {
+    if (two && first != 0 && second == 0 && size > 1) sure = false;
+    return first + (two ? second : 0u);
+  };
+  if (gl < 4) room.number[(sc.groups & ~3) + gl] = 0u;  // compared, as closed groups are
+  // the rank of a value among the groups': exact ones go by index where they are equal,
+  // others are two roundings of a step each from the sums
+  auto keep = [&](uint32_t mine, int g) __attribute__((always_inline)) {
+    int before = 0, near = 0;
+    for (int i = 0; i < sc.groups; i += 4) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(room.number + i);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        before += v[q] + (i + q < g ? 1u : 0u) > mine;
+        near += v[q] - mine + 2u <= 4u;
+      }
+    }
+    if (!exact && mine != 0 && near > 1) sure = false;
+    return mine != 0 && before < sc.top_groups;
+  };
+  if (size % C == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0) {
+    // a group is `lanes` lanes next to each other
+    uint32_t first = 0, second = 0;
+    auto merge = [&](uint32_t f, uint32_t s) __attribute__((always_inline)) {
+      second = max(min(first, f), max(second, s));
+      first = max(first, f);
+    };
+#pragma unroll
+    for (int j = 0; j < C; ++j) merge(key[j], 0u);
+    if (lanes >= 2) merge(dpp_u<kDppXor1>(first), dpp_u<kDppXor1>(second));
+    if (lanes >= 4) merge(dpp_u<kDppXor2>(first), dpp_u<kDppXor2>(second));
+    if (lanes >= 8) merge(dpp_u<kDppHalfMirror>(first), dpp_u<kDppHalfMirror>(second));
+    if (lanes >= 16) merge(dpp_u<kDppMirror>(first), dpp_u<kDppMirror>(second));
+    const int g = gl / lanes;
+    const uint32_t mine = g < sc.groups ? value(first, second) : 0u;
+    if (g < sc.groups) room.number[g] = mine;  // the group's lanes write the same
+    room_written();
+    kept = keep(mine, g) ? ~0u : 0u;
+  } else {
+    uint32_t* keys = room.key;
+#pragma unroll
+    for (int j = 0; j < C; ++j) keys[gl * C + j] = key[j];
+    room_written();
+    for (int g = gl; g < sc.groups; g += G) {
+      uint32_t first = 0, second = 0;
+      for (int i = 0; i < size; ++i) {
+        const uint32_t v = keys[g * size + i];
+        second = max(second, min(first, v));
+        first = max(first, v);
+      }
+      room.number[g] = value(first, second);
+    }
+    room_written();
+    for (int g = gl; g < sc.groups; g += G) room.index[g] = keep(room.number[g], g);
+    room_written();
+    read_kept<G, C>(a, size, room, kept);
+  }
+  return sure;
+}
+
+// The k largest of x, the lowest index first among equals: as route_token and
+// route_token_keys choose.  Lane gl < k receives the index of choice gl, -1 if there is none.
+template <typename In, int G, int C>
+__device__ __forceinline__ int choose_logits(float (&x)[C], int k) {
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  int choice = -1;
+  if constexpr (std::is_same_v<In, uint16_t>) {
+    uint32_t key[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) key[j] = route_key(x[j], gl * C + j);
+    for (int i = 0; i < k; ++i) {
+      uint32_t v = key[0];
+#pragma unroll
+      for (int j = 1; j < C; ++j) v = max(v, key[j]);
+      const uint32_t best = lanes_max<G>(v);
+      if (gl == i && best) choice = (int)(kMaxExperts - 1) - (int)(best & 0xffffu);
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (key[j] == best) key[j] = 0;
+    }
+  } else {
+    for (int i = 0; i < k; ++i) {
+      float v = x[0];
+      int bj = 0;
+#pragma unroll
+      for (int j = 1; j < C; ++j)
+        if (x[j] > v) v = x[j], bj = j;
+      const float best = group_max<G>(v);
+      const unsigned long long group = (G == 64 ? ~0ull : ((1ull << (G & 63)) - 1)) << (lane & ~(G - 1));
+      const int winner = __ffsll(__ballot(v == best) & group) - 1;
+      const int index = __shfl(gl * C + bj, winner);
+      if (gl == i && best > kNegInf) choice = index;
+      if (lane == winner)
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+          if (j == bj) x[j] = kNegInf;
+    }
+  }
+  return choice;
+}
+
+// The same of whole numbers, closed places 0; `sure` becomes false where two of them that meet
+// are equal.  The lane's keys hold j in their last bits, so the largest names its place
+// in the lane, and are sorted once: a choice then takes a lane's first one away.
+template <int G, int C>
+__device__ __forceinline__ int choose_numbers(const uint32_t (&number)[C], int k, bool& sure) {
+  static_assert((C & (C - 1)) == 0 && (((uint64_t)C) << kScoreBits) <= (1ull << 32), "key");
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  uint32_t key[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) key[j] = number[j] ? number[j] * C + (C - 1 - j) : 0u;
+  // odd-even merge sort, largest first
+#pragma unroll
+  for (int p = 1; p < C; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int i = q % p; i + q < C; i += 2 * q)
+#pragma unroll
+        for (int j = 0; j < q; ++j)
+          if (i + j + q < C && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t hi = max(key[i + j], key[i + j + q]), lo = min(key[i + j], key[i + j + q]);
+            key[i + j] = hi;
+            key[i + j + q] = lo;
+          }
+  int choice = -1;
+  uint32_t last = 0;
+  for (int i = 0;; ++i) {
+    const uint32_t best = lanes_max<G>(key[0]);
+    if (best != 0 && best / C == last / C) sure = false;
+    if (i == k) break;
+    last = best;
+    const unsigned long long vote = __ballot(key[0] == best);
+    const uint32_t mine = G == 64 ? 0u : (uint32_t)(vote >> (lane & 32)) >> (lane & 31 & ~(G - 1));
+    const int winner = G == 64 ? __ffsll(vote) - 1 : __ffs(mine) - 1;  // lane of the token's
+    if (gl == i && best) choice = winner * C + (int)(C - 1 - best % C);
+    // (selected by bits: a choice between array elements becomes a chain of comparisons)
+    const uint32_t take = gl == winner ? ~0u : 0u;
+#pragma unroll
+    for (int j = 0; j + 1 < C; ++j) key[j] = (key[j + 1] & take) | (key[j] & ~take);
+    key[C - 1] &= ~take;
+  }
+  return choice;
+}
+
+// The definition in 64 bits, on the c in `room`: which of the lane's experts have a kept group, ...
+template <int G, int C>
+__device__ __forceinline__ void keep_scores(const RouteArgs& a, const RouteScore& sc,
+                                            ScoreRoom<G * C>& room, uint32_t& kept) {
+  const int gl = threadIdx.x & (G - 1), size = a.E / sc.groups;
+  for (int g = gl; g < sc.groups; g += G) {
+    double first = kNegInfD, second = kNegInfD;
+    for (int i = 0; i < size; ++i) {
+      const double v = room.c[g * size + i];
+      second = larger(second, v < first ? v : first);
+      first = larger(first, v);
+    }
+    room.value[g] = sc.group_best == 2 && second > kNegInfD ? first + second : first;
+  }
+  room_written();
+  for (int g = gl; g < sc.groups; g += G) {
+    const double value = room.value[g];
+    int before = 0;
+    for (int i = 0; i < sc.groups; ++i) {
+      const double v = room.value[i];
+      before += v > value || (v == value && i < g);
+    }
+    room.index[g] = before < sc.top_groups;
+  }
+  room_written();
+  read_kept<G, C>(a, size, room, kept);
+}
+// ... and the k largest are chosen.
+template <int G, int C>
+__device__ __forceinline__ int choose_scores(double (&c)[C], int k) {
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  int choice = -1;
+  for (int i = 0; i < k; ++i) {
+    double v = c[0];
+    int bj = 0;
+#pragma unroll
+    for (int j = 1; j < C; ++j)
+      if (c[j] > v) v = c[j], bj = j;
+    const double best = lanes_fold<G>(v, larger);
+    const unsigned long long group = (G == 64 ? ~0ull : ((1ull << (G & 63)) - 1)) << (lane & ~(G - 1));
+    const int winner = __ffsll(__ballot(v == best) & group) - 1;
+    const int index = __shfl(gl * C + bj, winner);
+    if (gl == i && best > kNegInfD) choice = index;
+    if (lane == winner)
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j == bj) c[j] = kNegInfD;
+  }
+  return choice;
+}
 
 // As route_token.
-template <typename In, int G, int C>
-__device__ __forceinline__ void route_token_scored(const RouteArgs& a, const RouteScore& sc, int t,
-                                                   bool in, ScoreRoom<G * C>& room,
-                                                   int32_t& expert, float& weight) {
-  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+template <typename In, int G, int C, bool SIGMOID>
+__device__ __forceinline__ void route_token_scored(const RouteArgs& a, const Scores<SIGMOID>& sc,
+                                                   const ScoreLane<C>& sl, int t, bool in,
+                                                   ScoreRoom<G * C>& room, int32_t& expert,
+                                                   float& weight) {
+  const int gl = threadIdx.x & (G - 1);
   float x[C];
   load_logits<C>((const In*)a.logits + (size_t)(in ? t : 0) * a.E, in ? a.E : 0, gl * C, a.vec, x);
-  double s[C], c[C];
-  if (sc.sigmoid) {
-#pragma unroll
-    for (int j = 0; j < C; ++j) s[j] = 1.0 / (1.0 + exp(-(double)x[j]));
-  } else {
-    float m = x[0];
+  // softmax: the largest logit, and one over the sum where scores are compared or not divided by
+  // their own sum
+  const bool numbers = sc.bias || (sc.groups > 1 && sc.group_best == 2);
+  float m = 0.0f;
+  double over = 1.0;
+  if constexpr (!SIGMOID) {
+    m = x[0];
 #pragma unroll
     for (int j = 1; j < C; ++j) m = fmaxf(m, x[j]);
     m = group_max<G>(m);
     m = m > kNegInf ? m : 0.0f;
+  }
+  uint32_t key[C];
+  if (numbers || (!SIGMOID && !a.renorm)) {
+    double s[C];
     double total = 0.0;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      s[j] = x[j] == m ? 1.0 : exp((double)x[j] - (double)m);
-      total += s[j];
+      s[j] = score_of<SIGMOID>(x[j], m);
+      if constexpr (!SIGMOID) total += s[j];
     }
-    total = group_fold<G>(total, [](double u, double v) { return u + v; });
-#pragma unroll
-    for (int j = 0; j < C; ++j) s[j] = total > 0.0 ? s[j] / total : 0.0;
-  }
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int e = gl * C + j;
-    const double v = s[j] + (sc.bias && e < a.E ? (double)sc.bias[e] : 0.0);
-    c[j] = x[j] > kNegInf && v == v ? v : kNegInfD;
-  }
-  if (sc.groups > 1) {
-    const int size = a.E / sc.groups;
-#pragma unroll
-    for (int j = 0; j < C; ++j) room.c[gl * C + j] = c[j];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    for (int g = gl; g < sc.groups; g += G) {
-      double first = kNegInfD, second = kNegInfD;
-      for (int i = 0; i < size; ++i) {
-        const double v = room.c[g * size + i];
-        second = larger(second, v < first ? v : first);
-        first = larger(first, v);
-      }
-      room.value[g] = sc.group_best == 2 && second > kNegInfD ? first + second : first;
+    if constexpr (!SIGMOID) {
+      total = lanes_fold<G>(total, sum_of);
+      over = total > 0.0 ? reciprocal_d(total) : 0.0;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const int e = gl * C + j;
-      if (e >= a.E) continue;
-      const int mine = e / size;
-      const double value = room.value[mine];
-      int before = 0;
-      for (int g = 0; g < sc.groups; ++g) {
-        const double v = room.value[g];
-        before += v > value || (v == value && g < mine);
-      }
-      if (before >= sc.top_groups) c[j] = kNegInfD;
+      const double c = s[j] * over + (double)sl.bias[j];
+      const bool open = x[j] > kNegInf && c > kNegInfD;  // a NaN is not
+      room.c[gl * C + j] = open ? c : kNegInfD;
+      key[j] = open ? (uint32_t)__builtin_fma(c, sl.steps, sl.first) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const uint32_t b = __builtin_bit_cast(uint32_t, x[j] == 0.0f ? 0.0f : x[j]);
+      key[j] = x[j] > kNegInf ? b ^ (uint32_t)((int)b >> 31 | (int)0x80000000) : 0u;
     }
   }
-  bool open = false;
-  for (int i = 0; i < a.k; ++i) {
-    double v = c[0], p = s[0];
-    int bj = 0;
-#pragma unroll
-    for (int j = 1; j < C; ++j)
-      if (c[j] > v) v = c[j], p = s[j], bj = j;
-    const double best = group_fold<G>(v, larger);
-    if (gl == i) open = best > kNegInfD;
-    const unsigned long long group = (G == 64 ? ~0ull : ((1ull << (G & 63)) - 1)) << (lane & ~(G - 1));
-    if (lane == __ffsll(__ballot(v == best) & group) - 1) {
-      room.index[i] = gl * C + bj;
-      room.picked[i] = p;
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-        if (j == bj) c[j] = kNegInfD;
-    }
+  uint32_t kept = ~0u;  // by bits
+  if (sc.groups > 1) {
+    const bool sure = keep_groups<G, C>(a, sc, key, !numbers, room, kept);
+    if (__ballot(!sure || (numbers && sl.steps == 0.0))) keep_scores<G, C>(a, sc, room, kept);
   }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  open = open && gl < a.k;
-  double p = open ? room.picked[gl] : 0.0;
-  expert = open ? room.index[gl] : -1;
+#pragma unroll
+  for (int j = 0; j < C; ++j) room.x[gl * C + j] = x[j];
+  int choice;
+  if (sc.bias) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) key[j] &= (uint32_t)((int)(kept << (31 - j)) >> 31);
+    bool sure = sl.steps != 0.0;
+    choice = choose_numbers<G, C>(key, a.k, sure);
+    if (__ballot(!sure)) {
+      double c[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) c[j] = (kept >> j) & 1u ? room.c[gl * C + j] : kNegInfD;
+      choice = choose_scores<G, C>(c, a.k);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) x[j] = (kept >> j) & 1u ? x[j] : kNegInf;
+    choice = choose_logits<In, G, C>(x, a.k);
+  }
+  room_written();
+  const bool open = gl < a.k && choice >= 0;
+  const float y = open ? room.x[choice] : kNegInf;
+  double p = (SIGMOID ? y > -709.0f : open) ? score_of<SIGMOID>(y, m) : 0.0;
+  expert = open ? choice : -1;
   if (a.renorm) {
-    const double total = group_fold<G>(p, [](double u, double v) { return u + v; });
-    p = total > 0.0 ? p / total : 0.0;
+    const double total = lanes_fold<G>(p, sum_of);
+    p = total > 0.0 ? p * reciprocal_d(total) : 0.0;
+  } else {
+    p *= over;
   }
   weight = open ? (float)(p * (double)sc.scale) : 0.0f;
 }
@@ -319,12 +642,15 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, const Score& sc
                                              int* picked, ScoreRoom<G * C>* rooms, int* hist,
                                              int* slots) {
   const int per = blockDim.x / G, gl = threadIdx.x & (G - 1), first = (int)threadIdx.x / G;
+  constexpr bool kScored = !std::is_same_v<Score, NoScore>;
+  [[maybe_unused]] std::conditional_t<kScored, ScoreLane<C>, NoScore> sl;
+  if constexpr (kScored) sl = score_lane<G, C>(a, score);
   for (int t = t0 + first; t - first < t1; t += per) {
     const bool in = t < t1;
     int32_t e;
     float w;
-    if constexpr (!std::is_same_v<Score, NoScore>)
-      route_token_scored<In, G, C>(a, score, t, in, rooms[first], e, w);
+    if constexpr (kScored)
+      route_token_scored<In, G, C>(a, score, sl, t, in, rooms[first], e, w);
     else if constexpr (std::is_same_v<In, uint16_t>)
       route_token_keys<G, C>(a, t, in, e, w);
     else
@@ -615,8 +941,10 @@ hipError_t launch_route(const void* logits, bool f32, float* weights, int32_t* e
 hipError_t launch_route_scored(const void* logits, bool f32, float* weights, int32_t* experts,
                                int32_t* offsets, int32_t* rows, void* ws, int T, int E, int k,
                                bool renorm, const RouteScore& score, hipStream_t stream) {
-  return launch_route_with(logits, f32, weights, experts, offsets, rows, ws, T, E, k, renorm, score,
-                           stream);
+  return score.sigmoid ? launch_route_with(logits, f32, weights, experts, offsets, rows, ws, T, E, k,
+                                           renorm, Scores<true>{score}, stream)
+                       : launch_route_with(logits, f32, weights, experts, offsets, rows, ws, T, E, k,
+                                           renorm, Scores<false>{score}, stream);
 }
 
 }  // namespace swiglu

@@ -520,7 +520,7 @@ typedef enum {
  *   weights [T, k]  fp32, scale s_i, divided by the sum of s over the chosen experts with
  *                   renormalize != 0 (0 where that sum is 0)
  * Scores, sums and comparisons are in 64 bits, so that what decides between two
- * experts is not how exp rounds.  A logit of -inf or NaN is masked off, and so is an
+ * experts is not how exp rounds; without a bias single scores are compared by their logits.  A logit of -inf or NaN is masked off, and so is an
  * expert whose c is -inf or NaN; a group without open experts is not kept.  In a
  * softmax an infinite largest logit shares the weight with its equals.  experts,
  * rows, offsets, the places left over, the workspace (swiglu_route_workspace_bytes),

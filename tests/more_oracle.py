@@ -8,7 +8,8 @@ from ops_oracle import F64, U32, sigmoid_gate
 
 
 def route_scored(logits, bias, k, score, renorm, scale, groups, top, best):
-    """(weights, experts, offsets, rows) of logits [T, E]."""
+    """(weights, experts, offsets, rows) of logits [T, E]; without a bias single scores are compared by
+    their logits."""
     x = logits.to(F64).numpy()
     b = np.zeros(x.shape[1]) if bias is None else bias.to(F64).numpy()
     T, E = x.shape
@@ -31,11 +32,14 @@ def route_scored(logits, bias, k, score, renorm, scale, groups, top, best):
                 part = sorted(c[g * size:(g + 1) * size], reverse=True)[:best]
                 part = [p for p in part if p > -np.inf]
                 value.append(sum(part) if part else -np.inf)
+                if bias is None and best == 1:
+                    value[-1] = v[g * size:(g + 1) * size].max()
             kept = sorted(range(groups), key=lambda g: (-value[g], g))[:top]
             for g in range(groups):
                 if g not in kept:
                     c[g * size:(g + 1) * size] = -np.inf
-        order = sorted((j for j in range(E) if c[j] > -np.inf), key=lambda j: (-c[j], j))[:k]
+        by = v if bias is None else c
+        order = sorted((j for j in range(E) if c[j] > -np.inf), key=lambda j: (-by[j], j))[:k]
         if not order:
             continue
         p = s[order]

@@ -79,7 +79,8 @@ def test_special_logits(handle, score):
     inf, nan, low = float("inf"), float("nan"), torch.finfo(BF).min
     rows = [[-inf] * 6, [nan] * 6, [nan, 1, -inf, 2, nan, 0], [inf, 1, inf, 2, 0, -inf], [low] * 6,
             [low, -inf, low, nan, -inf, -inf], [0.0, -0.0, 0.0, -0.0, 0.0, 0.0],
-            [3, 3, 3, 1, 3, 3], [30, -100, 0, 30, -100, 0], [-inf, -inf, -inf, 1, 2, nan]]
+            [3, 3, 3, 1, 3, 3], [30, -100, 0, 30, -100, 0], [-inf, -inf, -inf, 1, 2, nan],
+            [50, 60, 40, 70, 80, 60], [-800, -750, -720, -900, -708, -1000]]
     for dtype, renorm, k in itertools.product((F32, BF), (True, False), (1, 3, 6)):
         x = torch.tensor(rows, dtype=dtype)
         check(handle, x, None, k, score, renorm)
