@@ -37,6 +37,13 @@ struct Int8Args {
   int C;                   // 2N (gated) or N (plain)
 };
 
+// Two fp32 to bf16, nearest even, by one instruction.
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // Row of A of sorted row `pos`, -1 if the slot names no row of A.
 template <int OP>
 __device__ __forceinline__ int int8_a_row(const Int8Args& g, int pos) {
@@ -220,9 +227,9 @@ struct Int8Tile {
   __host__ __device__ static constexpr int swz(int row) {
     return (((row >> 2) & 1) << 1) | (((row >> 1) ^ (row >> 3)) & 1);
   }
-  // groups run for a tile: what the next one needs is asked for in the first and used two
-  // groups before the end; by expert the slots come before the loads that they address
-  static constexpr int kMinGroups = 2, kMinGroupsGrouped = 4;
+  // groups run for a tile: the last two load for the next one and neither is the first; by
+  // expert the next tile's slots, asked for in the first, come before the loads that they address
+  static constexpr int kMinGroups = 3, kMinGroupsGrouped = 4;
 };
 
 template <int OP, bool GROUPED, int BM, int BNW, int WGM, int WGN, int PARTS>
@@ -390,26 +397,28 @@ __global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, i
   // Sub-step B (32 k) of a group.  The even ones read the other sub-step of their stage;
   // the odd ones wait for the next stage, and behind the barrier (every wave has read this stage)
   // read the next one's first fragments and load the stage of the group after next in this one's
-  // place.  LIVE: the wave's blocks of rows that the tile has; LAST: the next stage is the next
-  // tile's.
-  auto step = [&](auto b_c, auto live_c, auto last_c, const Tile& o, const i32x4& rsW,
-                  const uint32_t* rows, int g, int lg, int slot) __attribute__((always_inline)) {
+  // place.  LIVE: the wave's blocks of rows that the tile has; KIND: the tile's first group, whose
+  // first sums start from zero, one in between, and the last two.
+  constexpr int kFirst = 0, kMiddle = 1, kBeforeLast = 2, kLast = 3;
+  auto step = [&](auto b_c, auto live_c, auto kind_c, const Tile& o, const i32x4& rsW,
+                  const uint32_t* rows, int lg, int slot) __attribute__((always_inline)) {
     constexpr int B = decltype(b_c)::value, SUB = B & 1, HALF = B >> 1, LIVE = decltype(live_c)::value;
-    constexpr bool LAST = decltype(last_c)::value && B == 3;
+    constexpr int KIND = decltype(kind_c)::value;
+    constexpr bool LAST = KIND == kLast && B == 3;  // the next stage is the next tile's
     constexpr int NMF = C::FW * LIVE, NFRAG = C::FW + (LAST ? C::FA : LIVE);
     if constexpr (SUB == 1) {
       wait_vmcnt<2 * C::LOADS>();
       __syncthreads();
       if constexpr (B == 1) {
-        if (GROUPED && g == 0 && nxt.rows > 0) load_slots(nxt, par ^ 1);
-        if (g == Gp - 2 && nxt.rows > 0) load_scales(nxt, par ^ 1);
+        if (GROUPED && KIND == kFirst && nxt.rows > 0) load_slots(nxt, par ^ 1);
+        if (KIND == kBeforeLast && nxt.rows > 0) load_scales(nxt, par ^ 1);
       }
     }
     const int turn = HALF == 1 && SUB == 1 ? (slot ? -C::GROUP : C::GROUP) : 0;
     const uint32_t na = fa + turn, nw = fw + turn;
     auto one = [&](auto q_c) __attribute__((always_inline)) {
       constexpr int Q = decltype(q_c)::value, i = Q / LIVE, j = Q % LIVE;
-      acc[i][j] = mfma32_i8(wf[SUB][i], af[SUB][j], acc[i][j]);
+      acc[i][j] = mfma32_i8(wf[SUB][i], af[SUB][j], KIND == kFirst && B == 0 ? i32x16{} : acc[i][j]);
 #pragma unroll
       for (int r = Q * NFRAG / NMF; r < (Q + 1) * NFRAG / NMF; ++r)
         frag(na, nw, SUB == 0 ? HALF : HALF ^ 1, SUB ^ 1, r);
@@ -447,89 +456,84 @@ __global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, i
   for (int t = first; t < end; t += stride) {
     nxt = locate(t + stride, cur.expert);
     w_nxt = GROUPED ? weights(nxt) : w_cur;
-#pragma unroll
-    for (int i = 0; i < C::FW; ++i)
-#pragma unroll
-      for (int j = 0; j < C::FA; ++j) acc[i][j] = i32x16{};
     const int blocks = (cur.rows + 31) / 32;
     const int live = (blocks - wm + WGM - 1) / WGM;
-    auto groups = [&](auto live_c) __attribute__((always_inline)) {
-      using No = std::integral_constant<bool, false>;
-      using Yes = std::integral_constant<bool, true>;
-      auto group = [&](auto last_c, const Tile& o, const i32x4& rsW, const uint32_t* rows, int g,
+    auto tile = [&](auto live_c) __attribute__((always_inline)) {
+      constexpr int LIVE = decltype(live_c)::value;
+      auto group = [&](auto kind_c, const Tile& o, const i32x4& rsW, const uint32_t* rows,
                        int lg) __attribute__((always_inline)) {
-        step(std::integral_constant<int, 0>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
-        step(std::integral_constant<int, 1>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
-        step(std::integral_constant<int, 2>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
-        step(std::integral_constant<int, 3>{}, live_c, last_c, o, rsW, rows, g, lg, slot);
+        step(std::integral_constant<int, 0>{}, live_c, kind_c, o, rsW, rows, lg, slot);
+        step(std::integral_constant<int, 1>{}, live_c, kind_c, o, rsW, rows, lg, slot);
+        step(std::integral_constant<int, 2>{}, live_c, kind_c, o, rsW, rows, lg, slot);
+        step(std::integral_constant<int, 3>{}, live_c, kind_c, o, rsW, rows, lg, slot);
         const int turn = slot ? -C::GROUP : C::GROUP;
         fa += turn;
         fw += turn;
         slot ^= 1;
       };
-      int g = 0;
-      for (; g < Gp - 2; ++g) group(No{}, cur, w_cur, off, g, g + 2);
+      group(std::integral_constant<int, kFirst>{}, cur, w_cur, off, 2);
+      for (int g = 1; g < Gp - 2; ++g) group(std::integral_constant<int, kMiddle>{}, cur, w_cur, off, g + 2);
       // the groups to load are the next tile's
 #pragma unroll
       for (int q = 0; q < C::A_LOADS; ++q) a_next[q] = a_offset(nxt, par ^ 1, q);
-      group(No{}, nxt, w_nxt, a_next, g, 0);
-      group(Yes{}, nxt, w_nxt, a_next, g + 1, 1);
-    };
-    if (C::FA >= 4 && live >= 4) {
-      if constexpr (C::FA >= 4) groups(std::integral_constant<int, 4>{});
-    } else if (C::FA >= 3 && live >= 3) {
-      if constexpr (C::FA >= 3) groups(std::integral_constant<int, 3>{});
-    } else if (C::FA >= 2 && live >= 2) {
-      if constexpr (C::FA >= 2) groups(std::integral_constant<int, 2>{});
-    } else {
-      groups(std::integral_constant<int, 1>{});
-    }
-    // Scales, SiLU(Gate) Up, stores.  Registers 4 q .. 4 q + 3 are weight rows 8 q + 4 h + 0
-    // .. 3 (h = lane / 32); the exchanges give a lane 8 output columns next to each other.
-    const float* sa = reinterpret_cast<const float*>(smem + C::SA_OFF + par * 4 * BM);
-    const uint8_t* sw = smem + C::SW_OFF + par * 4 * BNW;
-    const int* slots = reinterpret_cast<const int*>(smem + C::ROW_OFF + par * 4 * BM);
+      group(std::integral_constant<int, kBeforeLast>{}, nxt, w_nxt, a_next, 0);
+      group(std::integral_constant<int, kLast>{}, nxt, w_nxt, a_next, 1);
+      // Scales, SiLU(Gate) Up, stores, for each LIVE by itself (joined before, the sums would be
+      // moved).  Registers 4 q .. 4 q + 3 are weight rows 8 q + 4 h + 0 .. 3 (h = lane / 32); the
+      // exchanges give a lane 8 output columns next to each other.
+      const float* sa = reinterpret_cast<const float*>(smem + C::SA_OFF + par * 4 * BM);
+      const uint8_t* sw = smem + C::SW_OFF + par * 4 * BNW;
+      const int* slots = reinterpret_cast<const int*>(smem + C::ROW_OFF + par * 4 * BM);
 #pragma unroll
-    for (int j = 0; j < C::FA; ++j) {
-      const int r = (j * WGM + wm) * 32 + fr;
-      if ((j * WGM + wm) * 32 >= cur.rows) continue;  // as a wave
-      const float s = sa[r];
-      int row = cur.pos0 + r;
-      if constexpr (GROUPED && OP == I8_PLAIN) row = slots[r];
-      const bool there = r < cur.rows && row >= 0 && row < a.R;
-      uint16_t* y = a.Y + (size_t)(there ? row : 0) * a.N;
+      for (int j = 0; j < LIVE; ++j) {
+        const int r = (j * WGM + wm) * 32 + fr;
+        const float s = sa[r];
+        int row = cur.pos0 + r;
+        if constexpr (GROUPED && OP == I8_PLAIN) row = slots[r];
+        const bool there = r < cur.rows && row >= 0 && row < a.R;
+        uint16_t* y = a.Y + (size_t)(there ? row : 0) * a.N;
 #pragma unroll
-      for (int i = 0; i < C::FW; ++i) {
-        const i32x16& d = acc[i][j];
-        float p[16];
+        for (int i = 0; i < C::FW; ++i) {
+          const i32x16& d = acc[i][j];
+          float p[16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 c = *reinterpret_cast<const f32x4*>(sw + ((wn * C::FW + i) * 32 + 8 * q + 4 * fh) * 4);
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 c = *reinterpret_cast<const f32x4*>(sw + ((wn * C::FW + i) * 32 + 8 * q + 4 * fh) * 4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[4 * q + e] = (float)d[4 * q + e] * s * c[e];
-        }
-        if constexpr (OP == I8_GATED) {
-          uint32_t o[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            o[q] = pack_bf16x2(silu(p[4 * q]) * p[4 * q + 1], silu(p[4 * q + 2]) * p[4 * q + 3]);
-          swap_halves(o[0], o[2]);
-          swap_halves(o[1], o[3]);
-          const int col = (cur.tn * C::NW + wn * C::FW + i) * 16 + 8 * fh;
-          if (there && col < a.N) *reinterpret_cast<u32x4*>(y + col) = u32x4{o[0], o[2], o[1], o[3]};
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; q += 2) {
+            for (int e = 0; e < 4; ++e) p[4 * q + e] = (float)d[4 * q + e] * s * c[e];
+          }
+          if constexpr (OP == I8_GATED) {
             uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(p[4 * q + 2 * e], p[4 * q + 2 * e + 1]);
+            for (int q = 0; q < 4; ++q)
+              o[q] = two_bf16(silu(p[4 * q]) * p[4 * q + 1], silu(p[4 * q + 2]) * p[4 * q + 3]);
             swap_halves(o[0], o[2]);
             swap_halves(o[1], o[3]);
-            const int col = (cur.tn * C::NW + wn * C::FW + i) * 32 + 8 * (q + fh);
-            if (there && col < a.N) *reinterpret_cast<u32x4*>(y + col) = u32x4{o[0], o[1], o[2], o[3]};
+            const int col = (cur.tn * C::NW + wn * C::FW + i) * 16 + 8 * fh;
+            if (there && col < a.N) *reinterpret_cast<u32x4*>(y + col) = u32x4{o[0], o[2], o[1], o[3]};
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = two_bf16(p[4 * q + 2 * e], p[4 * q + 2 * e + 1]);
+              swap_halves(o[0], o[2]);
+              swap_halves(o[1], o[3]);
+              const int col = (cur.tn * C::NW + wn * C::FW + i) * 32 + 8 * (q + fh);
+              if (there && col < a.N) *reinterpret_cast<u32x4*>(y + col) = u32x4{o[0], o[1], o[2], o[3]};
+            }
           }
         }
       }
+    };
+    if (C::FA >= 4 && live >= 4) {
+      if constexpr (C::FA >= 4) tile(std::integral_constant<int, 4>{});
+    } else if (C::FA >= 3 && live >= 3) {
+      if constexpr (C::FA >= 3) tile(std::integral_constant<int, 3>{});
+    } else if (C::FA >= 2 && live >= 2) {
+      if constexpr (C::FA >= 2) tile(std::integral_constant<int, 2>{});
+    } else {
+      tile(std::integral_constant<int, 1>{});  // also a wave without rows: it loads and waits with the others
     }
     cur = nxt;
     w_cur = w_nxt;
@@ -642,9 +646,9 @@ __global__ __launch_bounds__(64 * NW) void int8_stream_kernel(Int8Args g, int nb
     if (out < 0 || out >= g.R) return;
     uint16_t* y = g.Y + (size_t)out * g.N;
     if constexpr (OP == I8_GATED)
-      *reinterpret_cast<uint32_t*>(y + c / 2) = pack_bf16x2(silu(p[0]) * p[1], silu(p[2]) * p[3]);
+      *reinterpret_cast<uint32_t*>(y + c / 2) = two_bf16(silu(p[0]) * p[1], silu(p[2]) * p[3]);
     else
-      *reinterpret_cast<u32x2*>(y + c) = u32x2{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])};
+      *reinterpret_cast<u32x2*>(y + c) = u32x2{two_bf16(p[0], p[1]), two_bf16(p[2], p[3])};
   };
   if constexpr (NW == 1) {
 #pragma unroll
@@ -751,7 +755,7 @@ static double int8_cost(const Int8Call& c, const Int8Plan& p) {
     t = std::max(n / cus, 1.0) * (double)((rows + p.bn) * groups * 128) / p.cu_rate + p.piece;
   } else {
     rows = (rows + 31) / 32 * 32;
-    groups = std::max(groups, c.grouped ? 4LL : 2LL);
+    groups = std::max(groups, c.grouped ? 4LL : 3LL);
     const double rounds = std::ceil(n / (cus * p.per_cu));
     const double here = std::min<double>(p.per_cu, std::ceil(n / (cus * rounds)));
     t = rounds * ((double)((rows + p.bn) * groups * 128) * here / p.cu_rate + p.piece);
