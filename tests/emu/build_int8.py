@@ -19,7 +19,19 @@ SLOTS = [
     (r"row = slots\[r\];",
      r"{ const int there = slots[r]; ::emu_use(&there, 4); row = r < cur.rows ? a.rows[cur.pos0 + r] : -1; }", 1),
 ]
-PLANTS = []
+# 1: the tile's ring waits for one stage fewer
+# 2: the kernel ends without draining the loads issued past its last tile
+# 3: the first tile's slots are read without the wait for them
+# 4: a tile's slots are asked for when its scales are
+PLANTS = [
+    (r"^      wait_vmcnt<2 \* C::LOADS>\(\);$",
+     "      if (::g_emu_plant == 1) wait_vmcnt<3 * C::LOADS>(); else wait_vmcnt<2 * C::LOADS>();"),
+    (r"^(  // the zero loads issued past the last tile still write LDS\n)  wait_vmcnt<0>\(\);$",
+     "\\1  if (::g_emu_plant != 2) wait_vmcnt<0>();"),
+    (r"^(    load_slots\(cur, 0\);\n)    wait_vmcnt<0>\(\);$", "\\1    if (::g_emu_plant != 3) wait_vmcnt<0>();"),
+    (r"KIND == kFirst && nxt.rows > 0\) load_slots",
+     "(::g_emu_plant == 4 ? KIND == kBeforeLast : KIND == kFirst) && nxt.rows > 0) load_slots"),
+]
 
 
 def rewrite(src: str) -> str:

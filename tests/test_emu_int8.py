@@ -29,6 +29,12 @@ MANY = [("--cus", 8, "grouped", gated, v, 40, 144, 2, 3, ",".join(["2"] * 70 + [
         for gated in (1, 0) for v in range(8)]
 OTHER = [("quantize", rows, k) for rows, k in ((5, 16), (6, 1024), (3, 1040), (2, 9008), (2, 20000), (2, 40000))] + \
     [("pack", *a) for a in ((1, 1, 16), (3, 40, 144), (2, 64, 256))]
+LANDS, FLIGHT = "while a DMA into it may land", "still in flight when its thread ends"
+WALK = ("--cus", 8, "grouped")
+SPANS = (264, 656, 3, 5, "300,1,0,600,140,70")
+PLANTED = [(("--plant", p, *WALK, 1, v, *SPANS), LANDS) for p in (1, 3, 4) for v in (4, 5, 6, 7)] + \
+    [(("--plant", 1, "--cus", 8, "dense", 0, v, 900, 648, 528), LANDS) for v in (4, 5, 6, 7)] + \
+    [(("--plant", 2, *WALK, 0, v, *SPANS), FLIGHT) for v in (4, 5, 6, 7)]
 
 
 @pytest.fixture(scope="module")
@@ -45,7 +51,7 @@ def runs(tmp_path_factory):
         r = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=300, env=env)
         return r.returncode, r.stdout + r.stderr
     with cf.ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
-        jobs = DENSE + GROUPED + WALKS + FEW + MANY + OTHER
+        jobs = DENSE + GROUPED + WALKS + FEW + MANY + OTHER + [p for p, _ in PLANTED]
         yield dict(zip(jobs, ex.map(run, jobs)))
 
 
@@ -77,3 +83,10 @@ def test_many_experts(runs):
 
 def test_quantisation_and_packing(runs):
     clean(runs, OTHER)
+
+
+@pytest.mark.parametrize("job,message", PLANTED, ids=lambda x: " ".join(map(str, x)) if isinstance(x, tuple) else "")
+def test_planted_mistakes_are_found(runs, job, message):
+    """build_int8.py plants them in the emulation's copy of the source."""
+    rc, out = runs[job]
+    assert rc != 0 and message in out, out[-3000:]

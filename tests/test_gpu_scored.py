@@ -160,3 +160,43 @@ def test_choice_without_bias_is_the_routers(handle):
     sw.swiglu_route(handle, x.cuda(), w2, e2, off2, rows2, ws, 900, 72, 5)
     torch.cuda.synchronize()
     assert torch.equal(e, e2.cpu()) and torch.equal(off, off2.cpu()) and torch.equal(rows, rows2.cpu())
+
+
+@pytest.mark.parametrize("T,E,k,groups,top,best", [(9000, 32, 4, 8, 3, 2), (20000, 16, 2, 1, 1, 1),
+                                                   (4100, 256, 8, 8, 4, 2)])
+def test_many_tokens(handle, T, E, k, groups, top, best):
+    """More tokens than the workgroups take in one pass."""
+    check(handle, logits(T, E, BF), biases(E), k, "sigmoid", True, 2.5, groups, top, best)
+
+
+def test_graph_replays_equal_eager(handle):
+    T, E, k = 700, 64, 6
+    x, b = torch.empty(T, E, device="cuda"), biases(E).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = [torch.empty(T, k, device="cuda"), torch.empty(T, k, **i32), torch.empty(E + 1, **i32),
+           torch.empty(T * k, **i32)]
+    ws = torch.empty(sw.swiglu_route_workspace_bytes(T, E, k), dtype=torch.uint8, device="cuda")
+
+    def step():
+        sw.swiglu_route_scored(handle, x, b, *out, ws, T, E, k, score=sw.SCORE_SIGMOID, groups=8,
+                               top_groups=4, group_best=2)
+    side = torch.cuda.Stream()
+    x.normal_()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        x.normal_()
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in out]
+        for t in (*out, ws):
+            t.view(torch.uint8).fill_(0x7f)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(want, out)), i
