@@ -771,6 +771,19 @@ constexpr long long kRouteSmall = 512;
 
 // ---- one workgroup does everything -------------------------------------------------
 constexpr int kSmallThreads = 512;
+// Spans and sorted slots of the n choices in `slots`, by one workgroup of up to kSmallThreads;
+// hist holds the experts' counts, next zeros.
+__device__ __forceinline__ void route_sort(const RouteArgs& a, int* slots, int n, int* hist,
+                                           int* offset, int* next) {
+  const RouteShare share = route_share(slots, 0, n);
+  route_count(a, slots, share, next);
+  route_scan(hist, offset, a.E);
+  __syncthreads();
+  route_bases<kSmallThreads / 64>(next, offset, nullptr, a.E);
+  for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = offset[i];
+  __syncthreads();
+  route_place(a, slots, share, 0, n, offset[a.E], next);
+}
 template <typename In, int G, int C, typename Score>
 __global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a, Score score) {
   constexpr bool kScored = !std::is_same_v<Score, NoScore>;
@@ -786,14 +799,28 @@ __global__ __launch_bounds__(kSmallThreads) void route_small_kernel(RouteArgs a,
   __syncthreads();
   route_tokens<In, G, C>(a, score, 0, a.T, picked, rooms, hist, slots);
   __syncthreads();
-  const RouteShare share = route_share(slots, 0, n);
-  route_count(a, slots, share, next);
-  route_scan(hist, offset, a.E);
+  route_sort(a, slots, n, hist, offset, next);
+}
+
+// ---- few slots, many tokens for one workgroup: a wave's tokens a workgroup, then one sorts --
+// The choices are read back from `experts`, so no workspace is needed.
+template <int EMAX>
+__global__ __launch_bounds__(kSmallThreads) void route_sort_kernel(RouteArgs a) {
+  __shared__ __attribute__((aligned(16))) int next[kSmallThreads / 64 * EMAX];
+  __shared__ __attribute__((aligned(16))) int hist[EMAX];
+  __shared__ __attribute__((aligned(16))) int offset[EMAX + 1];
+  __shared__ __attribute__((aligned(16))) int slots[kRouteSmall];
+  const int nw = blockDim.x >> 6, n = a.T * a.k;
+  for (int i = threadIdx.x; i < nw * a.E; i += blockDim.x) next[i] = 0;
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
-  route_bases<kSmallThreads / 64>(next, offset, nullptr, a.E);
-  for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.offsets[i] = offset[i];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int x = a.experts[i];
+    slots[i] = x;
+    if (x >= 0) atomicAdd(&hist[x], 1);
+  }
   __syncthreads();
-  route_place(a, slots, share, 0, n, offset[a.E], next);
+  route_sort(a, slots, n, hist, offset, next);
 }
 
 // ---- many tokens: choose and count, then place ---------------------------------------
@@ -816,6 +843,7 @@ __global__ __launch_bounds__(kSelectThreads) void route_select_kernel(RouteArgs 
   const int t0 = blockIdx.x * a.tokens;
   route_tokens<In, G, C>(a, score, t0, min(t0 + a.tokens, a.T), picked, rooms, hist, nullptr);
   __syncthreads();
+  if (stride == 0) return;  // counted by the launch that sorts
   for (int i = threadIdx.x; i < a.E; i += blockDim.x)
     a.counts[(size_t)blockIdx.x * stride + i] = hist[i];
 }
@@ -906,9 +934,23 @@ long long route_workspace_bytes(long long T, long long E, long long k) {
 
 template <typename In, int G, int C, typename Score>
 static hipError_t launch_route_as(RouteArgs a, const Score& score, hipStream_t stream) {
+  constexpr bool kScored = !std::is_same_v<Score, NoScore>;
   if ((long long)a.T * a.k <= kRouteSmall) {
     // as many waves as the tokens fill: a token alone takes 4.2 us, with all 8 waves 4.8
     const int threads = std::max(64, std::min((a.T * G + 63) / 64 * 64, kSmallThreads));
+    // A scored choice takes that one compute unit 4 to 8 us a pass, so beyond one pass a wave's
+    // tokens are a workgroup and a second launch sorts: 256 experts in 8 groups, 8 choices, 16
+    // tokens 9.9 / 9.5 us (one launch / two), 24 13.9 / 9.5, 64 22.4 / 9.5, one choice of 512
+    // tokens 89.4 / 8.3; 64 experts, 6 choices, 32 tokens 7.8 / 8.4, 48 10.8 / 8.2.
+    if (kScored && a.T * G > kSmallThreads) {
+      a.tokens = 64 / G;
+      const hipError_t e = launch_op(route_select_kernel<In, G, C, Score>,
+                                     dim3((a.T + a.tokens - 1) / a.tokens), dim3(64), stream, a,
+                                     score, 0);
+      if (e != hipSuccess) return e;
+      const int n = a.T * a.k;
+      return launch_op(route_sort_kernel<G * C>, dim3(1), dim3((n + 63) / 64 * 64), stream, a);
+    }
     return launch_op(route_small_kernel<In, G, C, Score>, dim3(1), dim3(threads), stream, a, score);
   }
   long long tokens;

@@ -74,6 +74,19 @@ def test_scored(handle, T, E, k, groups, top, best, dtype):
         check(handle, logits(T, E, dtype), bias, k, score, renorm, 2.5, groups, top, best)
 
 
+@pytest.mark.parametrize("E,k,groups,top,best", [(60, 1, 4, 2, 2), (128, 8, 8, 4, 2), (200, 3, 8, 3, 1),
+                                                 (256, 8, 8, 4, 2), (500, 7, 10, 4, 2), (1000, 2, 50, 20, 1)])
+def test_few_slots(handle, E, k, groups, top, best):
+    """Up to 512 slots, where one workgroup sorts: tokens that it scores by itself and, beyond one
+    pass of its lanes, those that others score."""
+    for T in sorted({8, 9, 16, 17, 32, 33, 64, 512 // k}):
+        if T * k <= 512:
+            check(handle, logits(T, E, BF if T % 2 else F32), biases(E), k, "sigmoid", True, 2.5, groups,
+                  top, best)
+            check(handle, logits(T, E, F32, masked=0.95), None, k, "softmax", False, 1.0, groups, top,
+                  best)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_special_logits(handle, score):
     inf, nan, low = float("inf"), float("nan"), torch.finfo(BF).min
