@@ -588,14 +588,17 @@ __device__ __forceinline__ void route_token_scored(const RouteArgs& a, const Sco
       total = lanes_fold<G>(total, sum_of);
       over = total > 0.0 ? reciprocal_d(total) : 0.0;
     }
+    if (numbers) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const double c = s[j] * over + (double)sl.bias[j];
-      const bool open = x[j] > kNegInf && c > kNegInfD;  // a NaN is not
-      room.c[gl * C + j] = open ? c : kNegInfD;
-      key[j] = open ? (uint32_t)__builtin_fma(c, sl.steps, sl.first) : 0u;
+      for (int j = 0; j < C; ++j) {
+        const double c = s[j] * over + (double)sl.bias[j];
+        const bool open = x[j] > kNegInf && c > kNegInfD;  // a NaN is not
+        room.c[gl * C + j] = open ? c : kNegInfD;
+        key[j] = open ? (uint32_t)__builtin_fma(c, sl.steps, sl.first) : 0u;
+      }
     }
-  } else {
+  }
+  if (!numbers) {  // logits, which tell all apart: whatever the sum above was needed for
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const uint32_t b = __builtin_bit_cast(uint32_t, x[j] == 0.0f ? 0.0f : x[j]);

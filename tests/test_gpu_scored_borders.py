@@ -1,0 +1,56 @@
+"""The scored router where a choice or a weight hangs on the last bits of a score, against its 64-bit
+definition."""
+import itertools
+
+import pytest
+import torch
+
+import gemm_epilogues_mlp_amd as sw
+from test_gpu_scored import BF, F32, biases, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def handle():
+    h = sw.swiglu_create(0)
+    yield h
+    sw.swiglu_destroy(h)
+
+
+def randn(*shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(sum(shape)))
+
+
+# ------------------------------------------------------------------------------ choice of groups
+# groups of 2, 7, 8, 15, 20 and 32 experts: a share of a lane, lanes next to each other, neither
+GROUPED = [(1, 8, 2, 4, 2), (40, 128, 8, 16, 3), (300, 160, 6, 8, 3), (4000, 160, 6, 8, 3),
+           (300, 256, 8, 8, 4), (200, 56, 5, 8, 4), (700, 60, 4, 4, 1), (100, 960, 8, 64, 9)]
+
+
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("T,E,k,groups,top", GROUPED)
+def test_groups_of_peaked_logits(handle, T, E, k, groups, top, best):
+    """Most scores are far below the largest one: groups that differ only in those are still told
+    apart, whether weights are renormalised or not."""
+    for renorm, bias in itertools.product((True, False), (None, biases(E))):
+        for dtype, size in ((F32, 10.0), (BF, 10.0), (F32, 30.0)):
+            check(handle, (size * randn(T, E)).to(dtype), bias, k, "softmax", renorm, 2.5, groups, top,
+                  best)
+
+
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("T,E,k,groups,top", GROUPED)
+def test_groups_of_nearly_equal_logits(handle, T, E, k, groups, top, best):
+    """Scores within 1e-10 of each other: one step of the whole numbers that stand for them."""
+    for score, renorm, base in itertools.product(("softmax", "sigmoid"), (True, False), (0.0, 1e-6)):
+        check(handle, base + 1e-9 * randn(T, E), None, k, score, renorm, 1.0, groups, top, best)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_groups_whose_best_scores_are_all_small(handle, renorm):
+    """One logit far above all others: the second group is the one of the next largest logit, not the
+    first of those whose scores are tiny."""
+    x = torch.tensor([[40.0, 0, 1, 0, 2, 0, 10, 0], [0.0, 1, 2, 3, 90, 4, 6, 5]])
+    for dtype, T in itertools.product((F32, BF), (1, 3, 300)):
+        check(handle, x.repeat(T, 1).to(dtype), None, 2, "softmax", renorm, 1.0, 4, 2, 1)
