@@ -279,14 +279,18 @@ __device__ __forceinline__ double reciprocal_d(double d) {
   r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
   return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
+// What logit x is below the largest one, m.
+__device__ __forceinline__ double softmax_below(float x, float m) {
+  constexpr float kMost = 3.402823466e38f;
+  return (double)fminf(x, kMost) - (double)fminf(m, kMost);
+}
 // The score of logit x, but for the division by the sum in a softmax (m its largest logit; an
 // infinite one shares the weight with its equals).  Below -709, where e^-x has no value, the
 // sigmoid is as there.
 template <bool SIGMOID>
 __device__ __forceinline__ double score_of(float x, float m) {
   if constexpr (SIGMOID) return reciprocal_d(1.0 + exp_d(-(double)fmaxf(x, -709.0f)));
-  constexpr float kMost = 3.402823466e38f;
-  return exp_d((double)fminf(x, kMost) - (double)fminf(m, kMost));
+  return exp_d(softmax_below(x, m));
 }
 
 // What stays the same from token to token: the biases of the lane's experts, and the
@@ -632,9 +636,22 @@ __device__ __forceinline__ void route_token_scored(const RouteArgs& a, const Sco
   room_written();
   const bool open = gl < a.k && choice >= 0;
   const float y = open ? room.x[choice] : kNegInf;
-  double p = (SIGMOID ? y > -709.0f : open) ? score_of<SIGMOID>(y, m) : 0.0;
   expert = open ? choice : -1;
+  bool some = true;
+  if constexpr (!SIGMOID) {
+    // The largest logit may be of an expert that the bias or its group left out.  Weights that are
+    // divided by their sum are taken relative to the largest chosen one, whose share is 1, unless all
+    // their scores are 0: e^-745.13 is the least that 64 bits round to something else.
+    if (a.renorm) {
+      const float most = group_max<G>(y);
+      some = softmax_below(most, m) > -745.1332191019411;
+      m = some ? most : m;
+    }
+  }
+  double p = open && some && (!SIGMOID || y > -709.0f) ? score_of<SIGMOID>(y, m) : 0.0;
   if (a.renorm) {
+    // a sum of sigmoids may be as small as one: moved to where its reciprocal has a value
+    if constexpr (SIGMOID) p *= 0x1p512;
     const double total = lanes_fold<G>(p, sum_of);
     p = total > 0.0 ? p * reciprocal_d(total) : 0.0;
   } else {

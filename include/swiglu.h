@@ -518,7 +518,9 @@ typedef enum {
  *   the largest value are kept, the lower index first among equals
  *   the k largest c of the kept groups are chosen, the lower index first among equals
  *   weights [T, k]  fp32, scale s_i, divided by the sum of s over the chosen experts with
- *                   renormalize != 0 (0 where that sum is 0)
+ *                   renormalize != 0 (0 where that sum is 0; in a softmax where exp(x_i - x_max)
+ *                   is 0 in 64 bits for each of them, and otherwise what is divided are the
+ *                   exponentials relative to the largest chosen logit)
  * Scores, sums and comparisons are in 64 bits, so that what decides between two
  * experts is not how exp rounds; without a bias single scores are compared by their logits.  A logit of -inf or NaN is masked off, and so is an
  * expert whose c is -inf or NaN; a group without open experts is not kept.  In a

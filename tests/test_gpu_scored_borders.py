@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import gemm_epilogues_mlp_amd as sw
-from test_gpu_scored import BF, F32, biases, check
+import ops_oracle as O
+from test_gpu_scored import BF, F32, biases, check, run
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +55,33 @@ def test_groups_whose_best_scores_are_all_small(handle, renorm):
     x = torch.tensor([[40.0, 0, 1, 0, 2, 0, 10, 0], [0.0, 1, 2, 3, 90, 4, 6, 5]])
     for dtype, T in itertools.product((F32, BF), (1, 3, 300)):
         check(handle, x.repeat(T, 1).to(dtype), None, 2, "softmax", renorm, 1.0, 4, 2, 1)
+
+
+# ------------------------------------------------------------------------------------- weights
+def weights(handle, x, bias, k, **kw):
+    args = dict(score="softmax", renorm=True, scale=1.0, groups=1, top=1, best=1) | kw
+    return run(handle, x, bias, k, **args)[:2]
+
+
+@pytest.mark.parametrize("below", [600.0, 700.0, 708.5, 709.5, 710.0, 720.0, 740.0, 744.0, 745.0, 746.0,
+                                   1000.0])
+def test_renormalised_weights_far_below_an_expert_left_out(handle, below):
+    """The bias closes the expert of the largest logit, and the chosen scores are as small as 64 bits
+    hold; a weight is 0 only where they are 0."""
+    inf = float("inf")
+    for dtype, T in itertools.product((F32, BF), (1, 20, 300)):
+        x = torch.tensor([[0.0, -below]]).to(dtype)
+        # as bf16 rounds it
+        check(handle, x.repeat(T, 1), torch.tensor([-inf, 0.0]), 1, "softmax")
+        check(handle, x.repeat(T, 1), torch.tensor([-inf, 0.0]), 1, "softmax", False)
+    # two chosen ones: their weights are those of the difference of their logits
+    for gap in (0.0, 0.5, 3.0):
+        x = torch.tensor([[0.0, -float("inf"), -below, -below - gap]])
+        for bias, kw in ((torch.tensor([-inf, 0.0, 0.0, 0.0]), {}),
+                         (torch.tensor([-2.0, 0.0, 0.0, 0.0]), dict(groups=2, top=1)),
+                         (torch.tensor([-2.0, 0.0, 0.0, 0.0]), dict(groups=2, top=1, best=2))):
+            w, e = weights(handle, x, bias, 2, **kw)
+            assert sorted(e[0].tolist()) == [2, 3] and (gap == 0.0 or below > 744 or int(e[0, 0]) == 2)
+            # e^-745.13 is the least that rounds to a value other than 0
+            want = torch.softmax(x[0, e[0].long()].double(), -1) if below < 745.13 else torch.zeros(2)
+            O.assert_close(w[0], want, 1e-12 * want, f"{below} {gap} {kw}", half=O.U32)
