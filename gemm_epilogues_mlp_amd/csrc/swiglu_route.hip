@@ -256,8 +256,10 @@ __device__ __forceinline__ double lanes_fold(double v, F f) {
 __device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
 __device__ __forceinline__ double sum_of(double a, double b) { return a + b; }
 
-// e^x for x <= 709, within some 2^-52: x = n ln 2 + r with |r| <= ln(2) / 2, the Taylor
-// polynomial of e^r to the 13th power (what is left out is below 2^-57), scaled by 2^n.
+// e^x for x <= 709 (x <= 797 with MOVE <= -128), within some 2^-52: x = n ln 2 + r with |r| <= ln(2) / 2, the Taylor
+// polynomial of e^r to the 13th power (what is left out is below 2^-57), scaled by 2^n; MOVE: times
+// 2^MOVE more.
+template <int MOVE = 0>
 __device__ __forceinline__ double exp_d(double x) {
   x = x > -760.0 ? x : -760.0;  // 0 from there on
   const double n = __builtin_rint(x * 1.4426950408889634);
@@ -271,7 +273,7 @@ __device__ __forceinline__ double exp_d(double x) {
                             1.0};
 #pragma unroll
   for (int i = 0; i < 13; ++i) p = __builtin_fma(p, r, f[i]);
-  return __builtin_ldexp(p, (int)n);
+  return __builtin_ldexp(p, (int)n + MOVE);
 }
 // 1 / d for a normal d: the hardware's estimate and two steps of Newton
 __device__ __forceinline__ double reciprocal_d(double d) {
@@ -285,11 +287,15 @@ __device__ __forceinline__ double softmax_below(float x, float m) {
   return (double)fminf(x, kMost) - (double)fminf(m, kMost);
 }
 // The score of logit x, but for the division by the sum in a softmax (m its largest logit; an
-// infinite one shares the weight with its equals).  Below -709, where e^-x has no value, the
-// sigmoid is as there.
+// infinite one shares the weight with its equals).  A sigmoid is 0 where e^-x has no value, from
+// the fp32 logit -709.78271484375 on; next to it 1 + e^-x has one and its reciprocal is too small
+// for the steps of Newton, which are therefore taken 2^128 away.
 template <bool SIGMOID>
 __device__ __forceinline__ double score_of(float x, float m) {
-  if constexpr (SIGMOID) return reciprocal_d(1.0 + exp_d(-(double)fmaxf(x, -709.0f)));
+  if constexpr (SIGMOID) {
+    const double r = reciprocal_d(0x1p-128 + exp_d<-128>(-(double)fmaxf(x, -710.0f)));
+    return r * (x > -709.78271484375f ? 0x1p-128 : 0.0);
+  }
   return exp_d(softmax_below(x, m));
 }
 
@@ -648,7 +654,7 @@ __device__ __forceinline__ void route_token_scored(const RouteArgs& a, const Sco
       m = some ? most : m;
     }
   }
-  double p = open && some && (!SIGMOID || y > -709.0f) ? score_of<SIGMOID>(y, m) : 0.0;
+  double p = open && some ? score_of<SIGMOID>(y, m) : 0.0;
   if (a.renorm) {
     // a sum of sigmoids may be as small as one: moved to where its reciprocal has a value
     if constexpr (SIGMOID) p *= 0x1p512;

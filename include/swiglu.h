@@ -507,7 +507,7 @@ swiglu_status_t swiglu_route(swiglu_handle_t h, const void* logits, float* weigh
 /* How swiglu_route_scored turns a logit x into a score. */
 typedef enum {
   SWIGLU_SCORE_SOFTMAX = 0, /* exp(x) over the sum of it over the token's open logits */
-  SWIGLU_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-x))                                      */
+  SWIGLU_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-x)), 0 where exp(-x) has no 64-bit value */
 } swiglu_score_t;
 
 /* swiglu_route with a score for each expert, a bias that only steers the choice

@@ -85,3 +85,18 @@ def test_renormalised_weights_far_below_an_expert_left_out(handle, below):
             # e^-745.13 is the least that rounds to a value other than 0
             want = torch.softmax(x[0, e[0].long()].double(), -1) if below < 745.13 else torch.zeros(2)
             O.assert_close(w[0], want, 1e-12 * want, f"{below} {gap} {kw}", half=O.U32)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoids_next_to_the_least(handle, renorm):
+    """Scores down to 1 / (1 + e^709.78), behind which e^-x has no 64-bit value and the score is 0."""
+    rows = [[-709.5] * 6, [-720.0, -709.5, -709.25, -800.0, -709.0, -708.75],
+            [-709.78271484375, -709.78265380859375, -709.75, -720.0, -709.78265380859375, -1000.0],
+            [-1000.0, -710.0, -709.0, -709.03125, -709.0625, -708.0],
+            [-800.0, -750.0, -720.0, -711.0, -710.0, -709.78271484375]]
+    for bias, k in itertools.product((None, torch.zeros(6)), (1, 2, 3, 6)):
+        check(handle, torch.tensor(rows), bias, k, "sigmoid", renorm)
+        check(handle, torch.tensor(rows * 100), bias, k, "sigmoid", renorm)
+        if k <= 4:
+            for best in (1, 2):
+                check(handle, torch.tensor(rows), bias, k, "sigmoid", renorm, 1.0, 3, 2, best)
