@@ -281,10 +281,11 @@ __device__ __forceinline__ double reciprocal_d(double d) {
   r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
   return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
-// What logit x is below the largest one, m.
+// What logit x is below the largest one, m; an infinite m counts as 1e39, which is above all finite
+// ones, and nothing is above m.
 __device__ __forceinline__ double softmax_below(float x, float m) {
-  constexpr float kMost = 3.402823466e38f;
-  return (double)fminf(x, kMost) - (double)fminf(m, kMost);
+  const double top = m < __builtin_inff() ? (double)m : 1e39;
+  return __builtin_fmin((double)x - top, 0.0);
 }
 // The score of logit x, but for the division by the sum in a softmax (m its largest logit; an
 // infinite one shares the weight with its equals).  A sigmoid is 0 where e^-x has no value, from
