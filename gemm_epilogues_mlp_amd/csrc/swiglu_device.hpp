@@ -73,14 +73,23 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // at lds_wave_base + 16 i (lds_wave_base is wave-uniform).  Issued as inline
 // assembly so the compiler does not add a conservative vmcnt(0) in front of
 // every LDS read; completion is tracked with wait_vmcnt<>() by the caller.
+//
+// The compiler counts no wait states for an instruction inside asm, so what
+// the load reads has to be there:
+// * The resource: a vector memory instruction may read a scalar register five
+//   states after a vector instruction wrote it at the earliest.  rsrc comes
+//   from make_rsrc, which makes it uniform once, before the loops, and is
+//   handed on as it is.  (Another readfirstlane here had the compiler keep it in
+//   vector registers and write its scalar copy one to four states before 181
+//   of the loads.)  Where a kernel makes resources as it goes, see lds_dma16_wait.
+// * M0, which holds the LDS base: one state after a scalar write, the s_nop.
+// Both are looked for in the built code by tests/test_lds_load_waits_cpu.py.
 __device__ __forceinline__ void lds_dma16(uint32_t lds_wave_base, uint32_t voffset, i32x4 rsrc) {
-  // both operands are wave-uniform by construction; readfirstlane makes that
-  // visible to the compiler where its divergence analysis cannot prove it
+  // wave-uniform by construction; readfirstlane makes that visible to the
+  // compiler where its divergence analysis cannot prove it
   lds_wave_base = __builtin_amdgcn_readfirstlane(lds_wave_base);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) rsrc[i] = __builtin_amdgcn_readfirstlane(rsrc[i]);
   // the compiler itself places the LDS base in M0 (the "{m0}" operand)
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds"
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                :
                : "v"(voffset), "s"(rsrc), "{m0}"(lds_wave_base)
                : "memory");

@@ -1664,7 +1664,9 @@ __device__ __forceinline__ void f8_tile(const uint8_t* __restrict__ A,
   // unrolled block, a compile-time constant, so a scale read is a per-lane
   // row base, a wave-uniform ring slot and an immediate.
   const int sca_base = a_row * 16 + h;         // + 512 q for activation fragment q
-  const int scw_base = (BM + w_row) * 16 + h;  // + 512 i for weight fragment i
+  // weight fragment i: + 512 i, and from the activations' row to the weights', which is the same in
+  // all lanes of a wave (as a second per-lane base it was one register more than the largest tile has)
+  const int scw_part = 16 * (BM + (wave_u % WGN) * C::WTW - (wave_u / WGN) * C::WTM);
   auto scale_slot = [&](int s) __attribute__((always_inline)) -> int {
     const bool up = kSync && s >= nk0;
     const int kt = up ? s - nk0 : s;
@@ -1719,7 +1721,7 @@ __device__ __forceinline__ void f8_tile(const uint8_t* __restrict__ A,
       }
       if constexpr (j == C::FA - 1) {
         readW(Next{}, i, wf[i]);
-        if constexpr (C::MX) scn[C::FA + i] = scale_at(nslot, scw_base, 512 * i + NB);
+        if constexpr (C::MX) scn[C::FA + i] = scale_at(nslot + scw_part, sca_base, 512 * i + NB);
       }
       if constexpr (q >= DBEGIN) {
 #pragma unroll
@@ -1774,7 +1776,7 @@ __device__ __forceinline__ void f8_tile(const uint8_t* __restrict__ A,
 #pragma unroll
   for (int i = 0; i < C::FW; ++i) {
     readW(std::integral_constant<int, 0>{}, i, wf[i]);
-    if constexpr (C::MX) scn[C::FA + i] = scale_at(scale_slot(0), scw_base, 512 * i);
+    if constexpr (C::MX) scn[C::FA + i] = scale_at(scale_slot(0) + scw_part, sca_base, 512 * i);
   }
   if constexpr (C::MX) pack_scales(sca[0], scw[0]);
 
