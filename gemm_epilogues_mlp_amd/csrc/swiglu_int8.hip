@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t int8_code(float c, float a, float r) {
 
 // One row by W waves of a workgroup of 4 or more waves, a thread holding CH chunks of 8
 // values from the load of the maximum to the store of the codes, so X is read once.  Bound
-// by memory: 8192 x 18944 in 78 us (6.0 TB/s of bf16 in and codes out); 16 x 3584 in 2.6, a launch.
+// by memory: 8192 x 18944 in 75 to 84 us (78: 6.0 TB/s of bf16 in and codes out); 16 x 3584 in 2.6, a launch.
 template <int W, int CH>
 __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void quantize_int8_kernel(
     const uint16_t* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S, int rows, int K) {
@@ -206,13 +206,13 @@ __global__ __launch_bounds__(256) void pack_int8_kernel(const uint8_t* __restric
 // let the newest 2 LOADS of a wave be in flight, and more loads in between only make them
 // reach further.
 //
-// 8192 x 18944 x 3584 gated in 904 to 930 us, 8192 x 3584 x 18944 plain in 440 to 450 (2.4 to 2.5
-// POP/s; a library product of 8192^3 reaches 2.05 here): 72 % of the cycles in the matrix pipes
-// at 1.46 GHz and 65 % at 1.73, whatever clock power leaves (a card that takes 1013 and 471
-// us); no bank conflicts.  LDS moves all of
+// From card to card 8192 x 18944 x 3584 gated takes 896 to 1024 us and 8192 x 3584 x 18944 plain 439
+// to 471 (2.2 to 2.5 POP/s; a library product of 8192^3 reaches 2.05 here): 72 % of the cycles in the
+// matrix pipes at 1.46 GHz and 65 % at 1.73, whatever clock power leaves (a card that takes 1013 and
+// 471 us); no bank conflicts.  LDS moves all of
 // its 128 bytes a clock while the pipes run (96 read, 32 written); four waves of 128 x 128
 // each read a third less but leave one wave a SIMD: 958 against 913 us.  By expert, 32760
-// rows on 32: 527 to 548 us (3584 x 4736) and 282 to 306 (2368 x 3584), where partial tiles, the
+// rows on 32: 514 to 566 us (3584 x 4736) and 280 to 313 (2368 x 3584), where partial tiles, the
 // stores (12 % of the plain one without them) and the last round weigh more.
 template <int BM, int BNW, int WGM, int WGN>
 struct Int8Tile {
@@ -563,8 +563,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void int8_tile_kernel(Int8Args a, i
 // A come in 64-byte pieces).  Its NW waves take every NW-th group of 128 k, D groups in
 // flight while one is multiplied.  The waves' sums are added in LDS: integers, so their order
 // does not matter.  16 x 18944 x 3584 gated in 23.7 us (5.8 TB/s), 32 rows on 64 experts, 1536 x
-// 3584, in 28.4 (6.2); 16 x 3584 x 18944 plain in 17.0 (4.0), where the 224 pieces each take in as
-// many bytes of A as of W.  (32x32x32 instructions, whose 32 rows of A come in 32-byte pieces: 26.6,
+// 3584, in 28.4 (6.2); 16 x 3584 x 18944 plain in 17.0 (4.0) among others of its kind and 18 to 20 by
+// itself in a trace, where the 224 pieces each take in as many bytes of A as of W.  (32x32x32 instructions, whose 32 rows of A come in 32-byte pieces: 26.6,
 // 36.3 and 28.4.)
 template <int OP, bool GROUPED, int MT, int NB, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void int8_stream_kernel(Int8Args g, int nblk) {
@@ -729,7 +729,8 @@ static hipError_t launch_int8_tile(const Int8Call& c, const Int8Args& g, hipStre
 // Fitted to 90 calls of 1 to 21264 rows, dense and on 4 to 96 experts (each timed in
 // every variant): the choice is 1.6 % off the fastest in the mean, 30 % once (223 rows on 8
 // experts, 1200 x 1712: 10.5 us for the 64 x 128 tile, 8.1 streaming), 19 % at 764 x 728 x 6736
-// (26.7 and 22.4).
+// (26.7 and 22.4) and 14 to 20 % at 64 x 18944 x 3584 gated (38.9 to 41.1 us for the 64 x 128 tile,
+// 34.1 for the 128 x 256 one).
 struct Int8Plan {
   int bm, bn, per_cu;
   double launch, piece, cu_rate, weight_rate;

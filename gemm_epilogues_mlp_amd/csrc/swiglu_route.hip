@@ -192,7 +192,7 @@ __device__ __forceinline__ void route_token_keys(const RouteArgs& a, int t, bool
 // a choice are not told apart (equal logits, or chance: some 1e-7 a pair), the wave takes
 // the 64-bit path.  Without a bias the logits themselves are in the order of the scores.
 // What is left is instructions: some 950 vector ones of a wave for its two tokens of 256
-// experts, a third of them the exponentials (14 to 15 us to choose in two passes, 6.8 to 7.2 to
+// experts, a third of them the exponentials (13 to 15 us to choose in two passes, 5.6 to 7.2 to
 // place; 1024 threads a workgroup, one pass: 15.6).  One token: 7.7 us a call, a chain of 1500
 // instructions of one wave.
 struct NoScore {};

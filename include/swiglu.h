@@ -522,8 +522,9 @@ typedef enum {
  *                   is 0 in 64 bits for each of them, and otherwise what is divided are the
  *                   exponentials relative to the largest chosen logit)
  * Scores, sums and comparisons are in 64 bits, so that what decides between two
- * experts is not how exp rounds; without a bias single scores are compared by their logits.  A logit of -inf or NaN is masked off, and so is an
- * expert whose c is -inf or NaN; a group without open experts is not kept.  In a
+ * experts is not how exp rounds; without a bias single scores are compared by
+ * their logits.  A logit of -inf or NaN is masked off, and so is an expert whose c
+ * is -inf or NaN; a group without open experts is not kept.  In a
  * softmax an infinite largest logit shares the weight with its equals.  experts,
  * rows, offsets, the places left over, the workspace (swiglu_route_workspace_bytes),
  * the limits and the errors are swiglu_route's.  Also INVALID_ARG: E not a

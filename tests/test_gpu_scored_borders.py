@@ -104,11 +104,11 @@ def test_sigmoids_next_to_the_least(handle, renorm):
 
 @pytest.mark.parametrize("renorm", [True, False])
 def test_an_infinite_logit_next_to_the_largest_finite_one(handle, renorm):
-    """Only other infinite logits share the weight with it."""
+    """Only other infinite logits share the weight with it, also where the bias leaves them out."""
     inf, most = float("inf"), torch.finfo(F32).max
     rows = [[most, inf, 1.0, most, inf, 0.0], [most, most, 0.0, -most, 1e38, most], [inf, -inf, most, 0, 1, 2]]
-    for bias, k in itertools.product((None, torch.zeros(6), torch.tensor([0, .5, 0, -.5, 0, .25])),
-                                     (1, 3, 4)):
+    for bias, k in itertools.product((None, torch.zeros(6), torch.tensor([0, .5, 0, -.5, 0, .25]),
+                                      torch.tensor([0, -inf, 0, 0, -inf, 0])), (1, 3, 4)):
         check(handle, torch.tensor(rows), bias, k, "softmax", renorm)
         for best in (1, 2):
             check(handle, torch.tensor(rows), bias, k, "softmax", renorm, 1.0, 3, 2, best)
